@@ -265,6 +265,115 @@ PQG_API int pqg_quant_varlen(const void *in, void *out, void *scales,
               int64_t expected_m, pqg_stream_t stream);
 
 /*
+ * pqg_rmsnorm_quant — residual addition, root-mean-square norm and
+ * quantization of M rows of K elements in one pass: the producer of a
+ * block-scaled GEMM's input, without a 16-bit norm output in memory.  The
+ * scale rules, codes and layouts are pqg_quant's (and pqg_quant_nvfp4's).
+ * Per row:
+ *   h_i  = x_i + residual_i, one fp32 addition rounded to in_dtype (h = x
+ *          without a residual); stored to residual_out when it is not NULL
+ *   inv  = 1 / sqrt(sum_i h_i^2 / K + eps), evaluated in 64 bits and rounded
+ *          once to fp32.  A 64-bit sum does not depend on the order of its
+ *          terms at fp32 precision, so a row's codes do not depend on how
+ *          many rows the call has or on how a row is split
+ *   y_i  = (h_i * inv) * weight_i, two fp32 roundings; y is what is quantized
+ *          and is not rounded to 16 bits
+ *   FP32 scales: s = amax * c, one fp32 multiplication by the fp32 constant c
+ *          nearest 1 / 448 (E4M3) or 1 / 127 (INT8); codes from fp32(y / s)
+ * Codes, scales and h are bit-identical to that definition.
+ *
+ * in       device [M][K] of in_dtype, 32-byte aligned.
+ * residual device [M][K] of in_dtype or NULL, 32-byte aligned.
+ * weight   device [K] of in_dtype, 32-byte aligned.
+ * residual_out  device [M][K] of in_dtype or NULL, 32-byte aligned; may be
+ *          `residual` (or `in`) itself, but must not overlap it in part.
+ * out, scales, M, K, group, in_dtype, out_dtype, scale_fmt, scale_layout:
+ *          as for pqg_quant with one expert; K a multiple of 16, at most
+ *          16384.  With PQG_SCALE_E4M3 (group 16, PQG_E2M1) global_scale is
+ *          the device fp32 g of pqg_quant_nvfp4, else it is NULL.
+ * eps      finite, >= 0.  (eps = 0 and an all-zero row: inv is infinite, y is
+ *          not a number and its codes are unspecified; nothing faults.)
+ * Returns as pqg_quant.
+ */
+PQG_API int pqg_rmsnorm_quant(const void *in, const void *residual, const void *weight,
+              void *residual_out, void *out, void *scales, const float *global_scale,
+              int64_t M, int64_t K, int group, double eps, int in_dtype, int out_dtype,
+              int scale_fmt, int scale_layout, pqg_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged 4-bit key/value cache
+ * ------------------------------------------------------------------------ */
+
+enum pqg_kv_format {
+    PQG_KV_MXFP4 = 0, /* E2M1 codes, groups of 32 along the head dimension,
+                         UE8M0 scales                                       */
+    PQG_KV_NVFP4 = 1  /* E2M1 codes, blocks of 16, E4M3 block scales under
+                         one fp32 global scale each for keys and values     */
+};
+
+/*
+ * A cache: num_pages pages of page_size token slots.  Slot s is offset
+ * s % page_size of page s / page_size.  G is 32 (MXFP4) or 16 (NVFP4).
+ *   codes  [num_pages][kv_heads][page_size][head_dim / 2] bytes, two codes per
+ *          byte, element 2i in bits 0-3: the bytes pqg_quant (MXFP4) or
+ *          pqg_quant_nvfp4 writes for the row
+ *   scales [num_pages][kv_heads][head_dim / G][page_size] bytes: a group's
+ *          scales of neighbouring tokens are neighbours, so that a reader
+ *          fetches those of 4 or 8 tokens at once
+ * The struct is read by the host during a call; its pointers are device
+ * pointers, 16-byte aligned, and the buffers must not overlap.
+ */
+typedef struct pqg_kv_cache {
+    void *k_codes;
+    void *v_codes;
+    void *k_scales;
+    void *v_scales;
+    const float *global_scale; /* NVFP4: two floats, g of keys and g of values
+                                  (finite, > 0), 4-byte aligned; else NULL  */
+    int64_t num_pages;         /* num_pages * page_size < 2^31              */
+    int32_t page_size;         /* 16, 32, 64, 128 or 256                    */
+    int32_t kv_heads;          /* 1 ..= 1024                                */
+    int32_t head_dim;          /* 64, 128 or 256                            */
+    int32_t format;            /* pqg_kv_format                             */
+} pqg_kv_cache;
+
+/*
+ * pqg_kv_write — quantize the keys and values of T tokens into their slots.
+ *
+ * k, v     device [T][kv_heads][head_dim] of in_dtype, 32-byte aligned; the
+ *          rows of one token are dense, tokens are k_stride / v_stride
+ *          elements apart (a multiple of 16, at least kv_heads * head_dim), so
+ *          both may be slices of one projection's output.
+ * slots    device int32[T].  A token whose slot is negative or not below
+ *          num_pages * page_size is skipped (padding).  Slots of one call are
+ *          distinct; where two tokens name one slot, its contents are
+ *          unspecified.
+ * Slots that no token names keep their bytes.
+ */
+PQG_API int pqg_kv_write(const pqg_kv_cache *cache, const void *k, const void *v,
+              const int32_t *slots, int64_t T, int64_t k_stride, int64_t v_stride,
+              int in_dtype, pqg_stream_t stream);
+
+/*
+ * pqg_kv_read — the cached keys and values of B sequences as 16-bit rows.
+ * Row indptr[b] + j of k_out and v_out is token j of sequence b, its value
+ *   MXFP4: code * 2^(e - 127)                       rounded once to out_dtype
+ *   NVFP4: (code * sf) * (1 / g), in fp32, rounded once to out_dtype
+ *
+ * page_table  device int32[B][table_stride], of which max_pages columns are
+ *          used: token j of sequence b lies in page page_table[b][j / page_size].
+ *          A token whose page is not in [0, num_pages) reads as zeros.
+ * indptr   device int32[B + 1], not decreasing: sequence b has
+ *          indptr[b + 1] - indptr[b] tokens.  Rows of no sequence, and rows of
+ *          tokens past max_pages * page_size, are left as they are.
+ * k_out, v_out  device [M][kv_heads][head_dim] of out_dtype, dense, 32-byte
+ *          aligned.
+ */
+PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
+              int64_t table_stride, int64_t max_pages, const int32_t *indptr, int64_t B,
+              void *k_out, void *v_out, int64_t M, int out_dtype, pqg_stream_t stream);
+
+/*
  * pqg_scales_bytes — size in bytes of the scale buffer pqg_quant (or, for
  * PQG_SCALE_E4M3 with group 16, pqg_quant_nvfp4) writes for these arguments
  * (all experts, padding rows included).  Returns a negative pqg_status for
@@ -281,11 +390,12 @@ PQG_API const char *pqg_status_string(int status);
 PQG_API int pqg_last_cuda_error(void);
 
 /* Programmatic dependent launch (PDL) on (nonzero, the default) or off for
- * later pqg_quant calls of this process.  Returns the previous setting. */
+ * later calls of this process.  Returns the previous setting. */
 PQG_API int pqg_set_pdl(int enable);
 
-/* Number of kernels this process has launched through pqg_quant,
- * pqg_quant_nvfp4 and pqg_quant_varlen so far. */
+/* Number of kernels this process has launched through this library's entry
+ * points so far (pqg_kv_attention launches one or two per call, the others
+ * one). */
 PQG_API uint64_t pqg_launch_count(void);
 
 /* Library version string, e.g. "pqg 0.1.0 sm_100a". */

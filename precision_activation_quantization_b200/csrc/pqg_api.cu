@@ -12,6 +12,7 @@
 #include <cstdint>
 
 #include "pqg.h"
+#include "pqg_host.cuh"
 #include "pqg_launch.cuh"
 
 namespace {
@@ -24,13 +25,28 @@ constexpr int64_t kMaxDevices = 64;
 std::atomic<int> g_sm_count[kMaxDevices];
 int64_t padded_rows(int64_t M) { return (M + 3) / 4 * 4; }
 
-constexpr int64_t kMaxPerTokenK = 16384;
 constexpr int64_t kMaxSpecRows = 8;   // expected_m up to which masked calls load rows speculatively
 
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using pqg::aligned;
+using pqg::check_geometry;
+using pqg::kMaxPerTokenK;
+using pqg::overlaps;
 
-// Checks the enum values and sizes shared by pqg_quant and pqg_scales_bytes,
-// and returns the bytes of one expert's scale plane through *plane.
+}  // namespace
+
+namespace pqg {
+bool pdl_enabled() { return g_pdl.load(std::memory_order_relaxed) != 0; }
+
+int launched(cudaError_t err, int kernels) {
+    if (err != cudaSuccess) {
+        g_last_cuda_error = static_cast<int>(err);
+        (void)cudaGetLastError();  // the error is reported here; do not leave it sticky
+        return PQG_ERR_CUDA;
+    }
+    g_launches.fetch_add(static_cast<uint64_t>(kernels), std::memory_order_relaxed);
+    return PQG_OK;
+}
+
 int check_geometry(int64_t num_experts, int64_t M, int64_t K, int group, int scale_fmt,
                    int scale_layout, int64_t *plane) {
     if (scale_fmt != PQG_SCALE_FP32 && scale_fmt != PQG_SCALE_UE8M0 &&
@@ -74,14 +90,6 @@ int check_geometry(int64_t num_experts, int64_t M, int64_t K, int group, int sca
     return PQG_OK;
 }
 
-bool overlaps(const void *a, int64_t na, const void *b, int64_t nb) {
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-    return a0 < b0 + static_cast<uintptr_t>(nb) && b0 < a0 + static_cast<uintptr_t>(na);
-}
-
-}  // namespace
-
-namespace pqg {
 // magic and shift of div_segs (pqg_kernel.cuh): l = ceil(log2 segs),
 // magic = ceil(2^(31 + l) / segs), shift = l - 1; segs == 1 gives magic 0.
 void segs_divider(uint32_t segs, uint32_t *magic, uint32_t *shift) {
@@ -224,17 +232,10 @@ int quant_impl(const void *in, void *out, void *scales, const float *global_scal
         pqg::segs_divider(a.p.spec * a.p.segs, &a.p.spec_magic, &a.p.spec_shift);
     }
     a.fused = fuse_silu_mul != 0;
-    a.pdl = g_pdl.load(std::memory_order_relaxed) != 0;
+    a.pdl = pqg::pdl_enabled();
     a.stream = reinterpret_cast<cudaStream_t>(stream);
 
-    const cudaError_t err = in_dtype == PQG_BF16 ? pqg::launch_bf16(a) : pqg::launch_fp16(a);
-    if (err != cudaSuccess) {
-        g_last_cuda_error = static_cast<int>(err);
-        (void)cudaGetLastError();  // the error is reported here; do not leave it sticky
-        return PQG_ERR_CUDA;
-    }
-    g_launches.fetch_add(1, std::memory_order_relaxed);
-    return PQG_OK;
+    return pqg::launched(in_dtype == PQG_BF16 ? pqg::launch_bf16(a) : pqg::launch_fp16(a), 1);
 }
 
 }  // namespace

@@ -1,0 +1,137 @@
+// pqg_rmsnorm_quant: argument checks and launch.
+#include <algorithm>
+#include <cmath>
+
+#include "pqg.h"
+#include "pqg_host.cuh"
+#include "pqg_launch.cuh"
+#include "pqg_norm.cuh"
+
+namespace pqg {
+namespace {
+
+template <typename In, Kind KIND, int SLOTS>
+cudaError_t launch_norm_variant(const NormParams &p, cudaStream_t stream) {
+    auto kernel = rmsnorm_quant_kernel<In, KIND, SLOTS>;
+    int device = 0;
+    cudaError_t err = cudaGetDevice(&device);
+    if (err != cudaSuccess) return err;
+    static OccupancyCache cache;
+    const int bps = blocks_per_sm(cache, kernel, device, kNormThreads, 0u, 0u);
+    const int64_t rows_per_cta = (kNormThreads / 32) / p.wpr;
+    const int64_t ctas = std::min<int64_t>((p.M + rows_per_cta - 1) / rows_per_cta,
+                                           static_cast<int64_t>(sm_count(device)) * bps);
+    return launch(kernel, ctas, kNormThreads, 0, stream, p);
+}
+
+template <typename In, Kind KIND>
+cudaError_t launch_norm_slots(NormParams &p, cudaStream_t stream) {
+    // warps are added before slots: a row of 16384 elements is 8 warps x 4 slots
+    const uint32_t nslots = p.K / 16u;
+    uint32_t slots = 1;
+    p.wpr = 1;
+    while (p.wpr * 32u * slots < nslots) {
+        if (p.wpr < 8u) p.wpr *= 2;
+        else slots *= 2;
+    }
+    if (slots == 1) return launch_norm_variant<In, KIND, 1>(p, stream);
+    if (slots == 2) return launch_norm_variant<In, KIND, 2>(p, stream);
+    return launch_norm_variant<In, KIND, 4>(p, stream);
+}
+
+template <typename In>
+cudaError_t launch_norm(NormParams &p, Kind kind, cudaStream_t stream) {
+    switch (kind) {
+        case Kind::E4M3_FP32: return launch_norm_slots<In, Kind::E4M3_FP32>(p, stream);
+        case Kind::E4M3_UE8M0: return launch_norm_slots<In, Kind::E4M3_UE8M0>(p, stream);
+        case Kind::INT8_FP32: return launch_norm_slots<In, Kind::INT8_FP32>(p, stream);
+        case Kind::E2M1_UE8M0: return launch_norm_slots<In, Kind::E2M1_UE8M0>(p, stream);
+        case Kind::E2M1_E4M3: return launch_norm_slots<In, Kind::E2M1_E4M3>(p, stream);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+}  // namespace pqg
+
+extern "C" int pqg_rmsnorm_quant(const void *in, const void *residual, const void *weight,
+                                 void *residual_out, void *out, void *scales,
+                                 const float *global_scale, int64_t M, int64_t K, int group,
+                                 double eps, int in_dtype, int out_dtype, int scale_fmt,
+                                 int scale_layout, pqg_stream_t stream) {
+    using namespace pqg;
+    if (in_dtype != PQG_BF16 && in_dtype != PQG_FP16) return PQG_ERR_INVALID_ARG;
+    if (out_dtype != PQG_E4M3 && out_dtype != PQG_INT8 && out_dtype != PQG_E2M1)
+        return PQG_ERR_INVALID_ARG;
+    if (!(eps >= 0.0) || !std::isfinite(eps)) return PQG_ERR_INVALID_ARG;
+    const bool nvfp4 = scale_fmt == PQG_SCALE_E4M3;
+    if (nvfp4 != (global_scale != nullptr)) return PQG_ERR_INVALID_ARG;
+    int64_t plane = 0;
+    const int st = check_geometry(1, M, K, group, scale_fmt, scale_layout, &plane);
+    if (st != PQG_OK) return st;
+    if (nvfp4 && out_dtype != PQG_E2M1) return PQG_ERR_UNSUPPORTED;
+    if (scale_fmt == PQG_SCALE_UE8M0 && out_dtype == PQG_INT8) return PQG_ERR_UNSUPPORTED;
+    if (out_dtype == PQG_E2M1 && !nvfp4 &&
+        (scale_fmt != PQG_SCALE_UE8M0 || (group != 32 && group != 64 && group != 128)))
+        return PQG_ERR_UNSUPPORTED;
+    if (K % 16 != 0 || K > kMaxPerTokenK) return PQG_ERR_UNSUPPORTED;   // a row stays in registers
+    if (M == 0) return PQG_OK;
+
+    if (in == nullptr || weight == nullptr || out == nullptr || scales == nullptr)
+        return PQG_ERR_INVALID_ARG;
+    if (!aligned(in, 32) || !aligned(residual, 32) || !aligned(weight, 32) ||
+        !aligned(residual_out, 32) || !aligned(out, 16) || !aligned(global_scale, 4))
+        return PQG_ERR_ALIGNMENT;
+    if ((scale_fmt == PQG_SCALE_FP32 || scale_layout == PQG_UE8M0_PACKED ||
+         scale_layout == PQG_UE8M0_TILED_128x4) && !aligned(scales, 4))
+        return PQG_ERR_ALIGNMENT;
+
+    const int64_t rows = M * K * 2, weights = K * 2;
+    const int64_t out_row = out_dtype == PQG_E2M1 ? K / 2 : K, codes = M * out_row;
+    // every output against every input and against the other outputs
+    struct Buffer { const void *p; int64_t n; };
+    const Buffer reads[] = {{in, rows}, {residual, residual != nullptr ? rows : 0},
+                            {weight, weights}, {global_scale, nvfp4 ? 4 : 0}};
+    const Buffer writes[] = {{out, codes}, {scales, plane},
+                             {residual_out, residual_out != nullptr ? rows : 0}};
+    for (const Buffer &w : writes)
+        for (const Buffer &r : reads)
+            if (r.n > 0 && w.n > 0 && overlaps(w.p, w.n, r.p, r.n) &&
+                !(w.p == residual_out && w.p == r.p && r.n == rows && r.p != weight))
+                return PQG_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < i; ++j)
+            if (writes[i].n > 0 && writes[j].n > 0 &&
+                overlaps(writes[i].p, writes[i].n, writes[j].p, writes[j].n))
+                return PQG_ERR_INVALID_ARG;
+
+    NormParams p;
+    p.in = static_cast<const uint8_t *>(in);
+    p.residual = static_cast<const uint8_t *>(residual);
+    p.weight = static_cast<const uint8_t *>(weight);
+    p.residual_out = static_cast<uint8_t *>(residual_out);
+    p.out = static_cast<uint8_t *>(out);
+    p.scales = static_cast<uint8_t *>(scales);
+    p.gscale = global_scale;
+    p.eps = eps;
+    p.M = static_cast<uint32_t>(M);
+    p.K = static_cast<uint32_t>(K);
+    p.out_row_bytes = static_cast<uint32_t>(out_row);
+    p.ng = static_cast<uint32_t>(K / group);
+    // a group of 16, 32, 64 or 128 is 1, 2, 4 or 8 lanes; any other is the row
+    const bool lanes = group == 16 || group == 32 || group == 64 || group == 128;
+    p.group_lanes = lanes ? static_cast<uint32_t>(group) / 16u : 0u;
+    p.group_shift = 0;
+    while (lanes && (1u << p.group_shift) < p.group_lanes) ++p.group_shift;
+    p.mpad = static_cast<uint32_t>((M + 3) / 4 * 4);
+    p.layout = static_cast<uint32_t>(scale_layout);
+    p.wpr = 1;
+    const Kind kind = nvfp4                            ? Kind::E2M1_E4M3
+                      : out_dtype == PQG_E2M1          ? Kind::E2M1_UE8M0
+                      : scale_fmt == PQG_SCALE_UE8M0 ? Kind::E4M3_UE8M0
+                      : out_dtype == PQG_INT8        ? Kind::INT8_FP32
+                                                     : Kind::E4M3_FP32;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return launched(in_dtype == PQG_BF16 ? launch_norm<__nv_bfloat16>(p, kind, s)
+                                         : launch_norm<__half>(p, kind, s), 1);
+}

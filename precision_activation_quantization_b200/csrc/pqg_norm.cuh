@@ -1,0 +1,265 @@
+// Residual addition, root-mean-square norm and quantization in one pass, for
+// sm_100a.
+//
+// Mathematics.  h = x + r (rounded to the input type), inv = 1 / sqrt(mean(h^2)
+// + eps), y = (h inv) w, and y is quantized by groups as in pqg_kernel.cuh.
+// The sum of squares is kept in 64 bits: its value, rounded to fp32 inside inv,
+// is then the same in whatever order the terms are added, so a row's codes do
+// not depend on the launch shape, and an independent implementation meets the
+// same codes bit for bit.  One conversion and one 64-bit FMA per element fit
+// beside the memory traffic (an SM streams about 3.5 elements per clock here,
+// and its 64-bit pipe takes many more).
+//
+// A row stays in registers between the statistic and the quantization, so x and
+// r are read once and h and the codes are written once: 7 bytes per element
+// with a residual (bf16 in, one-byte codes), which HBM bounds.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "pqg_kernel.cuh"
+
+namespace pqg {
+
+struct NormParams {
+    const uint8_t *in;
+    const uint8_t *residual;   // or null
+    const uint8_t *weight;
+    uint8_t *residual_out;     // or null
+    uint8_t *out;
+    uint8_t *scales;
+    const float *gscale;       // NVFP4 only
+    double eps;
+    uint32_t M;
+    uint32_t K;
+    uint32_t out_row_bytes;
+    uint32_t ng;               // groups per row
+    uint32_t group_lanes;      // 16-element slots per group: 1, 2, 4, 8; 0: the whole row
+    uint32_t group_shift;      // log2(group_lanes)
+    uint32_t mpad;
+    uint32_t layout;
+    uint32_t wpr;              // warps per row: 1, 2, 4 or 8
+};
+
+constexpr int kNormThreads = 256;
+
+// Plain (coherent) 32-byte load: the residual may be updated in place.
+__device__ __forceinline__ void load32B_coherent(const void *p, uint32_t (&r)[8]) {
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void store32B(void *p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// Two fp32 values rounded to the 16-bit type (nearest even), `lo` in the low half.
+template <typename T>
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    uint32_t r;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// A group's scale.  The fp32 scales are amax times the fp32 constant nearest 1 /
+// FMAX, one rounding (at most an ulp from pqg_quant's quotient; y is not a
+// 16-bit value, so no unfused call gives the same bits anyway); the codes are
+// the rounding of fp32(y / s) for that s.  The other kinds as in make_scale.
+template <Kind KIND>
+__device__ __forceinline__ GroupScale make_norm_scale(float amax, const float *nv) {
+    if constexpr (KIND == Kind::E4M3_FP32 || KIND == Kind::INT8_FP32) {
+        GroupScale gs;
+        gs.s = __fmul_rn(fmaxf(amax, 1e-10f), KIND == Kind::INT8_FP32 ? kRcp127 : kRcp448);
+        gs.mult = __frcp_rn(gs.s);
+        gs.neg_s = -gs.s;
+        gs.e8 = 0;
+        return gs;
+    } else {
+        return make_scale<KIND>(amax, nv);
+    }
+}
+
+// Store the scale of group g of a row (the slot's first lane calls it; for the
+// word layouts `word` holds the exponents of groups 4j..4j+3).
+template <Kind KIND>
+__device__ __forceinline__ void store_norm_scale(const NormParams &p, uint32_t row, uint32_t g,
+                                                 const GroupScale &gs, uint32_t word) {
+    if (p.layout == kPacked) {
+        if ((g & 3u) == 0u)
+            reinterpret_cast<uint32_t *>(p.scales)[static_cast<uint64_t>(g >> 2) * p.mpad + row] =
+                word;
+    } else if (p.layout == kTiled128x4) {
+        store_tiled(p.scales, row, g, p.ng, gs.e8);
+    } else {
+        const uint64_t idx = p.layout == kRowMajor ? static_cast<uint64_t>(row) * p.ng + g
+                                                   : static_cast<uint64_t>(g) * p.mpad + row;
+        if constexpr (byte_scale(KIND))
+            p.scales[idx] = static_cast<uint8_t>(gs.e8);
+        else
+            reinterpret_cast<float *>(p.scales)[idx] = gs.s;
+    }
+}
+
+// A row is shared by p.wpr warps; a thread holds SLOTS slots of 16 consecutive
+// elements, neighbouring lanes holding neighbouring slots, so that a group is
+// 1 to 8 neighbouring lanes (or, per token, the whole row).
+template <typename In, Kind KIND, int SLOTS>
+__global__ void __launch_bounds__(kNormThreads)
+    rmsnorm_quant_kernel(const __grid_constant__ NormParams p) {
+    __shared__ double sums[2][kNormThreads / 32];
+    __shared__ float maxima[2][kNormThreads / 32];
+    __shared__ float nv[KIND == Kind::E2M1_E4M3 ? kNvTable : 1];
+
+    wait_for_producer();                        // before the first global access
+    if constexpr (KIND == Kind::E2M1_E4M3) {
+        Params q;
+        q.gscale = p.gscale;
+        build_nvfp4_table(q, nv);
+    }
+    const uint32_t lane = threadIdx.x & 31u;
+    const uint32_t warp = threadIdx.x >> 5;
+    const uint32_t wpr = p.wpr;
+    const uint32_t rows_per_iter = (kNormThreads / 32) / wpr;
+    const uint32_t sub = warp / wpr;            // this warp's row within the iteration
+    const uint32_t tpr = wpr * 32u;
+    const uint32_t tid = threadIdx.x - sub * tpr;   // thread index within the row
+    const uint32_t nslots = p.K / 16u;
+    const uint64_t row_bytes = static_cast<uint64_t>(p.K) * 2u;
+
+    uint32_t parity = 0;
+    for (uint32_t base = blockIdx.x * rows_per_iter; base < p.M;
+         base += gridDim.x * rows_per_iter, parity ^= 1u) {
+        const uint32_t row = base + sub;        // warp-uniform
+        const bool live = row < p.M;
+
+        // -- h = x + r, and this thread's share of its sum of squares -----------
+        uint32_t h[SLOTS][8];
+        double ss = 0.0;
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            const uint32_t slot = tid + j * tpr;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[j][i] = 0u;
+            if (live && slot < nslots) {
+                const uint64_t at = row * row_bytes + slot * 32u;
+                load32B_coherent(p.in + at, h[j]);
+                if (p.residual != nullptr) {
+                    uint32_t r[8];
+                    load32B_coherent(p.residual + at, r);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float a0, a1, b0, b1;
+                        widen2<In>(h[j][i], a0, a1);
+                        widen2<In>(r[i], b0, b1);
+                        h[j][i] = narrow2<In>(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
+                    }
+                }
+                if (p.residual_out != nullptr) store32B(p.residual_out + at, h[j]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float a0, a1;
+                widen2<In>(h[j][i], a0, a1);
+                ss = fma(static_cast<double>(a0), static_cast<double>(a0), ss);
+                ss = fma(static_cast<double>(a1), static_cast<double>(a1), ss);
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+        if (wpr > 1) {
+            if (lane == 0) sums[parity][warp] = ss;
+            asm volatile("bar.sync %0, %1;" ::"r"(1u + sub), "r"(wpr * 32u) : "memory");
+            ss = 0.0;
+            for (uint32_t w = 0; w < wpr; ++w) ss += sums[parity][sub * wpr + w];
+        }
+        const float inv = static_cast<float>(1.0 / sqrt(ss / p.K + p.eps));
+
+        // -- y, its groups' absmax, scales and codes ------------------------------
+        float row_max = 0.0f;                   // per token: over the whole row
+        if (p.group_lanes == 0u) {
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) {
+                const uint32_t slot = tid + j * tpr;
+                if (slot >= nslots) continue;
+                uint32_t w[8];
+                load32B(p.weight + slot * 32u, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float a0, a1, w0, w1;
+                    widen2<In>(h[j][i], a0, a1);
+                    widen2<In>(w[i], w0, w1);
+                    row_max = fmaxf(row_max, fabsf(__fmul_rn(__fmul_rn(a0, inv), w0)));
+                    row_max = fmaxf(row_max, fabsf(__fmul_rn(__fmul_rn(a1, inv), w1)));
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1)
+                row_max = fmaxf(row_max, __shfl_xor_sync(0xFFFFFFFFu, row_max, o));
+            if (wpr > 1) {
+                if (lane == 0) maxima[parity][warp] = row_max;
+                asm volatile("bar.sync %0, %1;" ::"r"(1u + sub), "r"(wpr * 32u) : "memory");
+                for (uint32_t w = 0; w < wpr; ++w)
+                    row_max = fmaxf(row_max, maxima[parity][sub * wpr + w]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+            const uint32_t slot = tid + j * tpr;
+            const bool ok = live && slot < nslots;
+            float y[16];
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 0u;
+            if (ok) load32B(p.weight + slot * 32u, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float a0, a1, w0, w1;
+                widen2<In>(h[j][i], a0, a1);
+                widen2<In>(w[i], w0, w1);
+                y[2 * i] = __fmul_rn(__fmul_rn(a0, inv), w0);
+                y[2 * i + 1] = __fmul_rn(__fmul_rn(a1, inv), w1);
+            }
+            float amax = row_max;
+            if (p.group_lanes != 0u) {
+                amax = absmax16(y);
+                for (uint32_t o = 1; o < p.group_lanes; o <<= 1)
+                    amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+            }
+            const GroupScale gs = make_norm_scale<KIND>(amax, nv);
+            uint32_t code[4];
+            // two quotient corrections: y has all 24 bits, and the one-correction
+            // quotient is proved for 16-bit inputs only
+            encode16<KIND, 2>(y, gs, code);
+
+            const uint32_t g = p.group_lanes == 0u ? 0u : slot >> p.group_shift;
+            uint32_t word = gs.e8;              // per token: bytes 1..3 are 0
+            if (p.layout == kPacked && p.group_lanes != 0u) {
+                // exponents of groups 4j..4j+3, from the 4 groups' lanes
+                word = ok ? gs.e8 << (8u * (g & 3u)) : 0u;
+                word |= __shfl_xor_sync(0xFFFFFFFFu, word, p.group_lanes);
+                word |= __shfl_xor_sync(0xFFFFFFFFu, word, 2u * p.group_lanes);
+            }
+            if (!ok) continue;
+            uint8_t *dst = p.out + static_cast<uint64_t>(row) * p.out_row_bytes;
+            if constexpr (is_e2m1(KIND))
+                store8B(dst + slot * 8u, code[0], code[1]);
+            else
+                store16B(dst + slot * 16u, code[0], code[1], code[2], code[3]);
+            const bool first = p.group_lanes == 0u ? tid == 0u && j == 0
+                                                   : (slot & (p.group_lanes - 1u)) == 0u;
+            if (first) store_norm_scale<KIND>(p, row, g, gs, word);
+        }
+    }
+    release_dependents();
+}
+
+}  // namespace pqg

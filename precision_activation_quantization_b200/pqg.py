@@ -15,6 +15,7 @@ and a scale-layout inference helper).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -29,6 +30,7 @@ PQG_ERR_CUDA = -4
 
 PQG_BF16, PQG_FP16, PQG_E4M3, PQG_INT8, PQG_E2M1 = 0, 1, 2, 3, 4
 PQG_SCALE_FP32, PQG_SCALE_UE8M0, PQG_SCALE_E4M3 = 0, 1, 2
+PQG_KV_MXFP4, PQG_KV_NVFP4 = 0, 1
 PQG_ROW_MAJOR, PQG_COL_MAJOR_TMA, PQG_UE8M0_PACKED, PQG_UE8M0_TILED_128x4 = 0, 1, 2, 3
 
 IN_DTYPES = {"bf16": PQG_BF16, "fp16": PQG_FP16}
@@ -36,10 +38,22 @@ OUT_DTYPES = {"e4m3": PQG_E4M3, "int8": PQG_INT8, "e2m1": PQG_E2M1}
 SCALE_FMTS = {"fp32": PQG_SCALE_FP32, "ue8m0": PQG_SCALE_UE8M0, "e4m3": PQG_SCALE_E4M3}
 LAYOUTS = {"row": PQG_ROW_MAJOR, "col": PQG_COL_MAJOR_TMA, "packed": PQG_UE8M0_PACKED,
            "tile128x4": PQG_UE8M0_TILED_128x4}
+KV_FORMATS = {"mxfp4": PQG_KV_MXFP4, "nvfp4": PQG_KV_NVFP4}
+KV_GROUP = {"mxfp4": 32, "nvfp4": 16}
 
-EXPORTS = ("pqg_quant", "pqg_quant_nvfp4", "pqg_quant_varlen", "pqg_scales_bytes",
+EXPORTS = ("pqg_quant", "pqg_quant_nvfp4", "pqg_quant_varlen", "pqg_rmsnorm_quant",
+           "pqg_kv_write", "pqg_kv_read", "pqg_scales_bytes",
            "pqg_status_string", "pqg_last_cuda_error", "pqg_set_pdl", "pqg_launch_count",
            "pqg_version")
+
+
+class pqg_kv_cache(ctypes.Structure):
+    """struct pqg_kv_cache of include/pqg.h."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("global_scale", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
 
 
 class PqgError(RuntimeError):
@@ -63,6 +77,14 @@ def _load() -> ctypes.CDLL:
     lib.pqg_quant_varlen.restype = i32
     lib.pqg_quant_varlen.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, i32, i32, i32, i32,
                                      i32, vp, vp, i64, vp]
+    lib.pqg_rmsnorm_quant.restype = i32
+    lib.pqg_rmsnorm_quant.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i64, i32,
+                                      ctypes.c_double, i32, i32, i32, i32, vp]
+    cache = ctypes.POINTER(pqg_kv_cache)
+    lib.pqg_kv_write.restype = i32
+    lib.pqg_kv_write.argtypes = [cache, vp, vp, vp, i64, i64, i64, i32, vp]
+    lib.pqg_kv_read.restype = i32
+    lib.pqg_kv_read.argtypes = [cache, vp, i64, i64, vp, i64, vp, vp, i64, i32, vp]
     lib.pqg_scales_bytes.restype = i64
     lib.pqg_scales_bytes.argtypes = [i64, i64, i64, i32, i32, i32]
     lib.pqg_status_string.restype = ctypes.c_char_p
@@ -111,6 +133,29 @@ def pqg_quant_varlen(in_ptr: int, out_ptr: int, scales_ptr: int, global_scale_pt
                                  K, group, in_dtype, out_dtype, scale_fmt, scale_layout,
                                  fuse_silu_mul, seg_indptr_ptr, seg_lens_ptr, expected_m,
                                  stream)
+
+
+def pqg_rmsnorm_quant(in_ptr: int, residual_ptr: int | None, weight_ptr: int,
+                      residual_out_ptr: int | None, out_ptr: int, scales_ptr: int,
+                      global_scale_ptr: int | None, M: int, K: int, group: int, eps: float,
+                      in_dtype: int, out_dtype: int, scale_fmt: int, scale_layout: int,
+                      stream: int | None) -> int:
+    return _lib.pqg_rmsnorm_quant(in_ptr, residual_ptr, weight_ptr, residual_out_ptr, out_ptr,
+                                  scales_ptr, global_scale_ptr, M, K, group, eps, in_dtype,
+                                  out_dtype, scale_fmt, scale_layout, stream)
+
+
+def pqg_kv_write(cache: pqg_kv_cache, k_ptr: int, v_ptr: int, slots_ptr: int, T: int,
+                 k_stride: int, v_stride: int, in_dtype: int, stream: int | None) -> int:
+    return _lib.pqg_kv_write(cache, k_ptr, v_ptr, slots_ptr, T, k_stride, v_stride, in_dtype,
+                             stream)
+
+
+def pqg_kv_read(cache: pqg_kv_cache, page_table_ptr: int, table_stride: int, max_pages: int,
+                indptr_ptr: int, B: int, k_out_ptr: int, v_out_ptr: int, M: int, out_dtype: int,
+                stream: int | None) -> int:
+    return _lib.pqg_kv_read(cache, page_table_ptr, table_stride, max_pages, indptr_ptr, B,
+                            k_out_ptr, v_out_ptr, M, out_dtype, stream)
 
 
 def pqg_scales_bytes(num_experts: int, M: int, K: int, group: int, scale_fmt: int,
@@ -363,3 +408,263 @@ def quant_varlen(x, seg_indptr, seg_lens=None, out=None, scales=None, *, group: 
     if st != PQG_OK:
         raise PqgError(st, "pqg_quant_varlen")
     return out, scales
+
+
+def _allocating_on(stream, device):
+    """Scope in which torch allocates from the pool of the stream a call runs on
+    (memory of another stream's pool may still be in use there)."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
+def _on_device(device, function, *args):
+    """Call a C entry point with ``device`` current."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        return function(*args)
+    with torch.cuda.device(device):
+        return function(*args)
+
+
+def rmsnorm_quant(x, weight, residual=None, out=None, scales=None, *, residual_out=None,
+                  eps: float = 1e-6, group: int = 128, out_dtype: str = "e4m3",
+                  scale_fmt: str = "fp32", layout: str = "row", global_scale=None, stream=None):
+    """Residual addition, RMS norm and quantization in one pass; returns
+    (out, scales, h).
+
+    ``x`` and ``residual`` are contiguous bf16/fp16 CUDA tensors [M, K] (or
+    [..., K], read as rows) and ``weight`` [K] of the same type.  h = x +
+    residual, rounded to their type, comes back in ``residual_out`` (pass
+    ``residual`` itself to update it in place; allocated when None); without a
+    residual h is ``x`` and nothing is stored.  The norm of h times ``weight``
+    is quantized by ``quant``'s rules into ``out`` [M, K] ([M, K/2] for E2M1)
+    and one plane of ``scales`` in the given layout; neither is written past its
+    rows.  NVFP4 is ``out_dtype="e2m1", scale_fmt="e4m3", group=16`` with
+    ``global_scale``.  The call runs with ``x``'s device current.
+    """
+    import torch
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"unsupported input dtype {x.dtype}")
+    if not x.is_cuda or not x.is_contiguous() or x.dim() < 2:
+        raise ValueError("x must be a contiguous CUDA tensor of rows")
+    K = x.shape[-1]
+    M = x.numel() // K if K else 0
+    dev = x.device
+    if (weight.dtype != x.dtype or weight.numel() != K or weight.device != dev
+            or not weight.is_contiguous()):
+        raise ValueError(f"weight must be a contiguous {x.dtype} tensor of {K} entries on "
+                         f"x's device")
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual: without one h is x")
+    else:
+        if residual_out is None:
+            with _allocating_on(stream, dev):
+                residual_out = torch.empty_like(x)
+        for name, t in (("residual", residual), ("residual_out", residual_out)):
+            if (t.dtype != x.dtype or t.numel() != x.numel() or t.device != dev
+                    or not t.is_contiguous()):
+                raise ValueError(f"{name} must be a contiguous {x.dtype} tensor of x's size on "
+                                 f"its device")
+    if out is None or scales is None:
+        with _allocating_on(stream, dev):
+            o, sc = allocate_outputs(M, K, group, out_dtype=out_dtype, scale_fmt=scale_fmt,
+                                     layout=layout, device=dev)
+        out = o[0] if out is None else out
+        scales = sc[0] if scales is None else scales
+    out_bytes = M * (K // 2 if out_dtype == "e2m1" else K)
+    if out.numel() * out.element_size() != out_bytes or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous buffer of {out_bytes} bytes")
+    nbytes = pqg_scales_bytes(1, M, K, group, SCALE_FMTS[scale_fmt], LAYOUTS[layout])
+    if (nbytes >= 0 and scales.numel() * scales.element_size() != nbytes) \
+            or not scales.is_contiguous():
+        raise ValueError(f"scales must be a contiguous buffer of {nbytes} bytes")
+    if not (out.device == scales.device == dev):
+        raise ValueError("x, out and scales must be on the same CUDA device")
+    gptr = None
+    if scale_fmt == "e4m3":
+        if (global_scale is None or global_scale.dtype != torch.float32
+                or global_scale.numel() != 1 or global_scale.device != dev):
+            raise ValueError("NVFP4 needs global_scale: a one-element fp32 tensor on x's device")
+        gptr = global_scale.data_ptr()
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    st = _on_device(dev, pqg_rmsnorm_quant, x.data_ptr(),
+                    None if residual is None else residual.data_ptr(), weight.data_ptr(),
+                    None if residual is None else residual_out.data_ptr(), out.data_ptr(),
+                    scales.data_ptr(), gptr, M, K, group, float(eps),
+                    PQG_BF16 if x.dtype == torch.bfloat16 else PQG_FP16, OUT_DTYPES[out_dtype],
+                    SCALE_FMTS[scale_fmt], LAYOUTS[layout], getattr(stream, "cuda_stream", stream))
+    if st != PQG_OK:
+        raise PqgError(st, "pqg_rmsnorm_quant")
+    return out, scales, x if residual is None else residual_out
+
+
+# ---- paged 4-bit key/value cache --------------------------------------------
+
+class KVCache:
+    """A paged 4-bit cache: its buffers and their geometry (see ``kv_cache``)."""
+
+    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "global_scale", "fmt", "device",
+                 "num_pages", "page_size", "kv_heads", "head_dim", "struct")
+
+
+def kv_cache(k_codes, v_codes, k_scales, v_scales, *, fmt: str = "mxfp4",
+             global_scale=None) -> KVCache:
+    """A cache over existing buffers.
+
+    Codes are uint8 CUDA tensors [num_pages, kv_heads, page_size, head_dim / 2]
+    and scales [num_pages, kv_heads, head_dim / G, page_size], contiguous, with
+    G = 32 for ``fmt="mxfp4"`` (UE8M0 scales) and 16 for "nvfp4" (E4M3 scales
+    under ``global_scale``, two fp32 values on the device: g of the keys and g of
+    the values).  The buffers belong to the caller, who keeps them alive.
+    """
+    import torch
+    if fmt not in KV_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(KV_FORMATS)}")
+    c = KVCache()
+    dev = k_codes.device
+    if k_codes.dim() != 4:
+        raise ValueError("codes must be [num_pages, kv_heads, page_size, head_dim / 2]")
+    pages, heads, size, half = k_codes.shape
+    want = {"k_codes": (pages, heads, size, half), "v_codes": (pages, heads, size, half)}
+    want["k_scales"] = want["v_scales"] = (pages, heads, 2 * half // KV_GROUP[fmt], size)
+    for name, t in (("k_codes", k_codes), ("v_codes", v_codes), ("k_scales", k_scales),
+                    ("v_scales", v_scales)):
+        if (t.dtype != torch.uint8 or tuple(t.shape) != want[name] or not t.is_contiguous()
+                or not t.is_cuda or t.device != dev):
+            raise ValueError(f"{name} must be a contiguous uint8 CUDA tensor {want[name]} on one "
+                             f"device")
+        setattr(c, name, t)
+    if (fmt == "nvfp4") != (global_scale is not None):
+        raise ValueError("global_scale (two fp32 values) goes with fmt='nvfp4'")
+    if global_scale is not None and (
+            global_scale.dtype != torch.float32 or global_scale.numel() != 2
+            or global_scale.device != dev or not global_scale.is_contiguous()):
+        raise ValueError("global_scale must be a contiguous fp32 tensor of two values on the "
+                         "cache's device")
+    c.global_scale, c.fmt, c.device = global_scale, fmt, dev
+    c.num_pages, c.kv_heads, c.page_size, c.head_dim = pages, heads, size, 2 * half
+    c.struct = pqg_kv_cache(
+        k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+        None if global_scale is None else global_scale.data_ptr(), pages, size, heads, 2 * half,
+        KV_FORMATS[fmt])
+    return c
+
+
+def kv_allocate(num_pages: int, page_size: int, kv_heads: int, head_dim: int, *,
+                fmt: str = "mxfp4", global_scale=None, device=None) -> KVCache:
+    """A new cache of zeros (see ``kv_cache``)."""
+    import torch
+    if fmt not in KV_FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(KV_FORMATS)}")
+    device = torch.device("cuda" if device is None else device)
+    codes = (num_pages, kv_heads, page_size, head_dim // 2)
+    scales = (num_pages, kv_heads, head_dim // KV_GROUP[fmt], page_size)
+    k, v, ks, vs = (torch.zeros(n, dtype=torch.uint8, device=device)
+                    for n in (codes, codes, scales, scales))
+    return kv_cache(k, v, ks, vs, fmt=fmt, global_scale=global_scale)
+
+
+def _token_stride(t, heads: int, dim: int, name: str, cache) -> int:
+    """Elements between the tokens of [T, heads, dim] with dense heads."""
+    import torch
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [tokens, {heads}, {dim}]")
+    if t.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on the cache's device")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"the heads of a token of {name} must be dense")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _index_tensor(t, name: str, cache, numel: int | None = None) -> int:
+    import torch
+    if (t.dtype != torch.int32 or t.device != cache.device or not t.is_contiguous()
+            or (numel is not None and t.numel() != numel)):
+        raise ValueError(f"{name} must be a contiguous int32 tensor"
+                         + ("" if numel is None else f" of {numel} entries")
+                         + " on the cache's device")
+    return t.data_ptr()
+
+
+def _page_table(t, cache):
+    """(address, row stride, columns, rows) of an int32 page table [B, max_pages]."""
+    import torch
+    if (t.dim() != 2 or t.dtype != torch.int32 or t.device != cache.device or t.shape[1] < 1
+            or (t.shape[1] > 1 and t.stride(1) != 1)):
+        raise ValueError("page_table must be an int32 tensor [sequences, pages] on the cache's "
+                         "device with dense rows")
+    rows, width = t.shape
+    return t.data_ptr(), t.stride(0) if rows > 1 else width, width, rows
+
+
+def kv_write(cache: KVCache, k, v, slots, *, stream=None) -> None:
+    """Quantize the keys and values of T tokens into their slots of the cache.
+
+    ``k`` and ``v`` are bf16/fp16 CUDA tensors [T, kv_heads, head_dim]; the heads
+    of a token are dense, tokens may be strided (slices of one projection's
+    output).  ``slots`` [T] int32 holds page * page_size + offset; a token with a
+    slot outside the cache (-1: padding) is skipped.  Slots of one call must be
+    distinct.
+    """
+    import torch
+    ks = _token_stride(k, cache.kv_heads, cache.head_dim, "k", cache)
+    vs = _token_stride(v, cache.kv_heads, cache.head_dim, "v", cache)
+    T = k.shape[0]
+    if v.shape[0] != T or v.dtype != k.dtype:
+        raise ValueError("k and v must hold the same tokens in the same dtype")
+    sp = _index_tensor(slots, "slots", cache, T)
+    if stream is None:
+        stream = torch.cuda.current_stream(cache.device)
+    st = _on_device(cache.device, pqg_kv_write, cache.struct, k.data_ptr(), v.data_ptr(), sp, T,
+                    ks, vs, PQG_BF16 if k.dtype == torch.bfloat16 else PQG_FP16,
+                    getattr(stream, "cuda_stream", stream))
+    if st != PQG_OK:
+        raise PqgError(st, "pqg_kv_write")
+
+
+def kv_read(cache: KVCache, page_table, indptr, num_tokens: int, *, dtype=None, k_out=None,
+            v_out=None, stream=None):
+    """The cached keys and values of B sequences as packed 16-bit rows; returns
+    (k, v), each [num_tokens, kv_heads, head_dim].
+
+    ``page_table`` [B, max_pages] int32 names the pages of each sequence and
+    ``indptr`` [B + 1] int32 the row its first token goes to.  Rows of no
+    sequence are left as they are (``torch.empty`` when allocated here);
+    tokens of a page outside the cache read as zeros.  ``dtype`` (bf16 by
+    default) is that of the tensors allocated here.
+    """
+    import torch
+    tp, stride, width, B = _page_table(page_table, cache)
+    ip = _index_tensor(indptr, "indptr", cache, B + 1)
+    shape = (num_tokens, cache.kv_heads, cache.head_dim)
+    given = k_out if k_out is not None else v_out
+    if given is not None and dtype not in (None, given.dtype):
+        raise ValueError("dtype differs from the given output's")
+    dtype = given.dtype if given is not None else dtype or torch.bfloat16
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"unsupported dtype {dtype}")
+    with _allocating_on(stream, cache.device):
+        k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
+        v_out = torch.empty(shape, dtype=dtype, device=cache.device) if v_out is None else v_out
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if (tuple(t.shape) != shape or t.dtype != dtype or t.device != cache.device
+                or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on the cache's "
+                             f"device")
+    if stream is None:
+        stream = torch.cuda.current_stream(cache.device)
+    st = _on_device(cache.device, pqg_kv_read, cache.struct, tp, stride, width, ip, B,
+                    k_out.data_ptr(), v_out.data_ptr(), num_tokens,
+                    PQG_BF16 if dtype == torch.bfloat16 else PQG_FP16,
+                    getattr(stream, "cuda_stream", stream))
+    if st != PQG_OK:
+        raise PqgError(st, "pqg_kv_read")
+    return k_out, v_out
