@@ -374,6 +374,49 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
               void *k_out, void *v_out, int64_t M, int out_dtype, pqg_stream_t stream);
 
 /*
+ * pqg_kv_attention — attention of the last q_len tokens of B sequences over
+ * the cache (decode: q_len = 1; several tokens: verification of drafts).  The
+ * tokens' own keys and values are in the cache already.  With n = seq_lens[b],
+ * clamped into [0, max_pages * page_size], token t of sequence b sees keys
+ * j < n - (q_len - 1 - t):
+ *   s_j = sm_scale * sum_d q_d K_jd,  out = sum_j softmax(s)_j V_j,
+ *   lse = log sum_j exp(s_j)
+ * A row that sees no key has out = 0 and lse = -infinity.  Keys in a page that
+ * is not in [0, num_pages) are not seen.
+ *
+ * q        device [B * q_len][q_heads][head_dim] of in_dtype (tokens of a
+ *          sequence together, oldest first), 16-byte aligned; tokens are
+ *          q_stride elements apart (a multiple of 8, at least q_heads *
+ *          head_dim), heads dense.  q_heads is a multiple of kv_heads; head h
+ *          reads key/value head h / (q_heads / kv_heads).
+ * page_table, table_stride, max_pages   as for pqg_kv_read.
+ * seq_lens device int32[B].
+ * out      device [B * q_len][q_heads][head_dim] of in_dtype, dense, 16-byte
+ *          aligned.
+ * lse      device fp32 [B * q_len][q_heads], or NULL.
+ * B, q_len, q_heads   B <= 2^20, q_len 1 ..= 1024, q_heads <= 16384.
+ * max_len  a hint for splitting the keys among thread blocks: the longest
+ *          sequence; <= 0 means max_pages * page_size.  Sequences longer than
+ *          the hint are computed in full.
+ * workspace, workspace_bytes   device scratch of at least
+ *          pqg_kv_attention_workspace(...) bytes for the same arguments,
+ *          16-byte aligned (NULL when that is 0).  Its contents are dead
+ *          after the call; calls that may run at the same time need one each.
+ * Keys and values are used exactly as stored; queries exactly; the softmax
+ * weights are rounded to 11 bits for the product with V, sums are in fp32.
+ */
+PQG_API int pqg_kv_attention(const pqg_kv_cache *cache, const void *q, int64_t q_stride,
+              const int32_t *page_table, int64_t table_stride, int64_t max_pages,
+              const int32_t *seq_lens, int64_t B, int64_t q_len, int64_t q_heads,
+              float sm_scale, int64_t max_len, void *out, float *lse, void *workspace,
+              int64_t workspace_bytes, int in_dtype, pqg_stream_t stream);
+
+/* Bytes of scratch pqg_kv_attention needs for these arguments, or a negative
+ * pqg_status for arguments it would reject. */
+PQG_API int64_t pqg_kv_attention_workspace(const pqg_kv_cache *cache, int64_t max_pages,
+              int64_t B, int64_t q_len, int64_t q_heads, int64_t max_len);
+
+/*
  * pqg_scales_bytes — size in bytes of the scale buffer pqg_quant (or, for
  * PQG_SCALE_E4M3 with group 16, pqg_quant_nvfp4) writes for these arguments
  * (all experts, padding rows included).  Returns a negative pqg_status for

@@ -1,0 +1,166 @@
+// pqg_kv_attention: argument checks, the plan of a call and its launches.
+#include "pqg_attention.cuh"
+
+#include <algorithm>
+#include <cmath>
+
+#include "pqg_cache_host.cuh"
+
+namespace pqg {
+
+int sm_count(int device);  // cached cudaDevAttrMultiProcessorCount
+
+namespace {
+
+// How a call is cut: row tiles per key/value head, keys per chunk, chunks.
+struct Plan {
+    int64_t rows, row_tiles, chunk, chunks, workspace;
+};
+
+constexpr int64_t kMinChunk = 256;
+constexpr int64_t kTargetBlocks = 148 * 16;
+
+int make_plan(const CacheView &c, int64_t max_pages, int64_t B, int64_t q_len, int64_t q_heads,
+              int64_t max_len, Plan *plan) {
+    if (B < 0 || B > kMaxSequences || q_len < 1 || q_len > kMaxQueryTokens || q_heads < 1 ||
+        q_heads % c.heads != 0 || q_heads > kMaxQueryHeads || max_pages < 1 ||
+        max_pages >= (int64_t{1} << 31))
+        return PQG_ERR_INVALID_ARG;
+    const int64_t cap = std::min<int64_t>(max_pages << c.page_shift, INT32_MAX);
+    const int64_t len = max_len > 0 && max_len < cap ? max_len : cap;
+    plan->rows = q_len * (q_heads / c.heads);
+    plan->row_tiles = (plan->rows + kAttentionThreads / 32 - 1) / (kAttentionThreads / 32);
+    const int64_t units = std::max<int64_t>(1, B * c.heads * plan->row_tiles);
+    int64_t chunks = std::max<int64_t>(1, kTargetBlocks / units);
+    chunks = std::min(chunks, (len + kMinChunk - 1) / kMinChunk);
+    plan->chunk = (len + chunks - 1) / chunks;
+    plan->chunk = (plan->chunk + 31) / 32 * 32;
+    plan->chunks = (len + plan->chunk - 1) / plan->chunk;
+    if (units * plan->chunks >= (int64_t{1} << 31)) return PQG_ERR_INVALID_ARG;
+    plan->workspace = 0;
+    if (plan->chunks > 1)
+        plan->workspace = B * c.heads * plan->chunks * plan->rows * (c.head_dim + 2) * 4;
+    return PQG_OK;
+}
+
+template <typename In, int G, int D>
+cudaError_t launch_attention(const AttentionParams &p, const Plan &plan, cudaStream_t stream,
+                             int *kernels) {
+    const int64_t blocks = static_cast<int64_t>(p.B) * p.c.heads * plan.row_tiles * plan.chunks;
+    cudaError_t err =
+        launch(attention_kernel<In, G, D>, blocks, kAttentionThreads, 0, stream, p);
+    *kernels = 1;
+    if (err != cudaSuccess || plan.chunks == 1) return err;
+    const int64_t joins = static_cast<int64_t>(p.B) * p.c.heads * p.rows;
+    *kernels = 2;
+    return launch(attention_join_kernel<In, G, D>,
+                  (joins + kAttentionThreads / 32 - 1) / (kAttentionThreads / 32),
+                  kAttentionThreads, 0, stream, p);
+}
+
+template <typename In, int G>
+cudaError_t launch_head_dim(const AttentionParams &p, const Plan &plan, cudaStream_t stream,
+                            int *kernels) {
+    switch (p.c.head_dim) {
+        case 64: return launch_attention<In, G, 64>(p, plan, stream, kernels);
+        case 128: return launch_attention<In, G, 128>(p, plan, stream, kernels);
+        case 256: return launch_attention<In, G, 256>(p, plan, stream, kernels);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+}  // namespace pqg
+
+extern "C" {
+
+int64_t pqg_kv_attention_workspace(const pqg_kv_cache *cache, int64_t max_pages, int64_t B,
+                                   int64_t q_len, int64_t q_heads, int64_t max_len) {
+    using namespace pqg;
+    CacheView c;
+    const int st = check_cache(cache, &c);
+    if (st != PQG_OK) return st;
+    Plan plan;
+    const int ps = make_plan(c, max_pages, B, q_len, q_heads, max_len, &plan);
+    return ps != PQG_OK ? ps : plan.workspace;
+}
+
+int pqg_kv_attention(const pqg_kv_cache *cache, const void *q, int64_t q_stride,
+                     const int32_t *page_table, int64_t table_stride, int64_t max_pages,
+                     const int32_t *seq_lens, int64_t B, int64_t q_len, int64_t q_heads,
+                     float sm_scale, int64_t max_len, void *out, float *lse, void *workspace,
+                     int64_t workspace_bytes, int in_dtype, pqg_stream_t stream) {
+    using namespace pqg;
+    AttentionParams p;
+    const int st = check_cache(cache, &p.c);
+    if (st != PQG_OK) return st;
+    if (in_dtype != PQG_BF16 && in_dtype != PQG_FP16) return PQG_ERR_INVALID_ARG;
+    const int ts = check_table(B, table_stride, max_pages);
+    if (ts != PQG_OK) return ts;
+    Plan plan;
+    const int ps = make_plan(p.c, max_pages, B, q_len, q_heads, max_len, &plan);
+    if (ps != PQG_OK) return ps;
+    const int64_t D = cache->head_dim, row = q_heads * D;
+    if (!std::isfinite(sm_scale) || q_stride < row || q_stride > kMaxStride)
+        return PQG_ERR_INVALID_ARG;
+    if (B == 0) return PQG_OK;
+    if (q == nullptr || page_table == nullptr || seq_lens == nullptr || out == nullptr)
+        return PQG_ERR_INVALID_ARG;
+    if (plan.workspace > 0 && (workspace == nullptr || workspace_bytes < plan.workspace))
+        return PQG_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || q_stride % 8 != 0 || !aligned(out, 16) || !aligned(lse, 4) ||
+        !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+        (plan.workspace > 0 && !aligned(workspace, 16)))
+        return PQG_ERR_ALIGNMENT;
+
+    const int64_t T = B * q_len;
+    struct Buffer { const void *p; int64_t n; };
+    const Buffer reads[] = {{q, ((T - 1) * q_stride + row) * 2},
+                            {page_table, ((B - 1) * table_stride + max_pages) * 4},
+                            {seq_lens, B * 4}};
+    const Buffer writes[] = {{out, T * row * 2}, {lse, lse != nullptr ? T * q_heads * 4 : 0},
+                             {workspace, plan.workspace}};
+    for (int i = 0; i < 3; ++i) {
+        if (writes[i].n == 0) continue;
+        if (overlaps_cache(cache, writes[i].p, writes[i].n)) return PQG_ERR_INVALID_ARG;
+        for (const Buffer &r : reads)
+            if (overlaps(writes[i].p, writes[i].n, r.p, r.n)) return PQG_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (writes[j].n > 0 && overlaps(writes[i].p, writes[i].n, writes[j].p, writes[j].n))
+                return PQG_ERR_INVALID_ARG;
+    }
+
+    p.q = static_cast<const uint8_t *>(q);
+    p.out = static_cast<uint8_t *>(out);
+    p.lse = lse;
+    p.part = static_cast<float *>(workspace);
+    p.stat = plan.workspace == 0
+                 ? nullptr
+                 : reinterpret_cast<float2 *>(p.part + B * p.c.heads * plan.chunks * plan.rows * D);
+    p.table = page_table;
+    p.seq_lens = seq_lens;
+    p.q_stride = static_cast<uint64_t>(q_stride);
+    p.table_stride = static_cast<uint64_t>(table_stride);
+    p.scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
+    p.max_pages = static_cast<uint32_t>(max_pages);
+    p.B = static_cast<uint32_t>(B);
+    p.q_len = static_cast<uint32_t>(q_len);
+    p.group = static_cast<uint32_t>(q_heads / p.c.heads);
+    p.rows = static_cast<uint32_t>(plan.rows);
+    p.row_tiles = static_cast<uint32_t>(plan.row_tiles);
+    p.chunk = static_cast<uint32_t>(plan.chunk);
+    p.chunks = static_cast<uint32_t>(plan.chunks);
+    const bool nv = cache->format == PQG_KV_NVFP4;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int kernels = 0;
+    cudaError_t err;
+    if (in_dtype == PQG_BF16)
+        err = nv ? launch_head_dim<__nv_bfloat16, 16>(p, plan, s, &kernels)
+                 : launch_head_dim<__nv_bfloat16, 32>(p, plan, s, &kernels);
+    else
+        err = nv ? launch_head_dim<__half, 16>(p, plan, s, &kernels)
+                 : launch_head_dim<__half, 32>(p, plan, s, &kernels);
+    return launched(err, kernels);
+}
+
+}  // extern "C"

@@ -10,6 +10,8 @@ namespace pqg {
 constexpr int64_t kMaxKvHeads = 1024;
 constexpr int64_t kMaxStride = int64_t{1} << 32;      // elements between tokens
 constexpr int64_t kMaxSequences = int64_t{1} << 20;
+constexpr int64_t kMaxQueryTokens = 1024;             // q_len
+constexpr int64_t kMaxQueryHeads = 16384;
 
 // Checks the cache's description and fills in the kernels' view of it.
 int check_cache(const pqg_kv_cache *cache, CacheView *view);

@@ -42,7 +42,8 @@ KV_FORMATS = {"mxfp4": PQG_KV_MXFP4, "nvfp4": PQG_KV_NVFP4}
 KV_GROUP = {"mxfp4": 32, "nvfp4": 16}
 
 EXPORTS = ("pqg_quant", "pqg_quant_nvfp4", "pqg_quant_varlen", "pqg_rmsnorm_quant",
-           "pqg_kv_write", "pqg_kv_read", "pqg_scales_bytes",
+           "pqg_kv_write", "pqg_kv_read", "pqg_kv_attention", "pqg_kv_attention_workspace",
+           "pqg_scales_bytes",
            "pqg_status_string", "pqg_last_cuda_error", "pqg_set_pdl", "pqg_launch_count",
            "pqg_version")
 
@@ -85,6 +86,11 @@ def _load() -> ctypes.CDLL:
     lib.pqg_kv_write.argtypes = [cache, vp, vp, vp, i64, i64, i64, i32, vp]
     lib.pqg_kv_read.restype = i32
     lib.pqg_kv_read.argtypes = [cache, vp, i64, i64, vp, i64, vp, vp, i64, i32, vp]
+    lib.pqg_kv_attention.restype = i32
+    lib.pqg_kv_attention.argtypes = [cache, vp, i64, vp, i64, i64, vp, i64, i64, i64,
+                                     ctypes.c_float, i64, vp, vp, vp, i64, i32, vp]
+    lib.pqg_kv_attention_workspace.restype = i64
+    lib.pqg_kv_attention_workspace.argtypes = [cache, i64, i64, i64, i64, i64]
     lib.pqg_scales_bytes.restype = i64
     lib.pqg_scales_bytes.argtypes = [i64, i64, i64, i32, i32, i32]
     lib.pqg_status_string.restype = ctypes.c_char_p
@@ -156,6 +162,21 @@ def pqg_kv_read(cache: pqg_kv_cache, page_table_ptr: int, table_stride: int, max
                 stream: int | None) -> int:
     return _lib.pqg_kv_read(cache, page_table_ptr, table_stride, max_pages, indptr_ptr, B,
                             k_out_ptr, v_out_ptr, M, out_dtype, stream)
+
+
+def pqg_kv_attention(cache: pqg_kv_cache, q_ptr: int, q_stride: int, page_table_ptr: int,
+                     table_stride: int, max_pages: int, seq_lens_ptr: int, B: int, q_len: int,
+                     q_heads: int, sm_scale: float, max_len: int, out_ptr: int,
+                     lse_ptr: int | None, workspace_ptr: int | None, workspace_bytes: int,
+                     in_dtype: int, stream: int | None) -> int:
+    return _lib.pqg_kv_attention(cache, q_ptr, q_stride, page_table_ptr, table_stride, max_pages,
+                                 seq_lens_ptr, B, q_len, q_heads, sm_scale, max_len, out_ptr,
+                                 lse_ptr, workspace_ptr, workspace_bytes, in_dtype, stream)
+
+
+def pqg_kv_attention_workspace(cache: pqg_kv_cache, max_pages: int, B: int, q_len: int,
+                               q_heads: int, max_len: int) -> int:
+    return _lib.pqg_kv_attention_workspace(cache, max_pages, B, q_len, q_heads, max_len)
 
 
 def pqg_scales_bytes(num_experts: int, M: int, K: int, group: int, scale_fmt: int,
@@ -668,3 +689,62 @@ def kv_read(cache: KVCache, page_table, indptr, num_tokens: int, *, dtype=None, 
     if st != PQG_OK:
         raise PqgError(st, "pqg_kv_read")
     return k_out, v_out
+
+
+def kv_attention(q, cache: KVCache, page_table, seq_lens, *, sm_scale: float | None = None,
+                 max_len: int = 0, out=None, lse=None, return_lse: bool = False, stream=None):
+    """Attention of each sequence's newest tokens over the cache; returns out, or
+    (out, lse) with ``return_lse`` or a given ``lse``.
+
+    ``q`` is a bf16/fp16 CUDA tensor [B * q_len, q_heads, head_dim], the q_len
+    newest tokens of a sequence together, oldest first; the heads of a token are
+    dense, tokens may be strided.  ``seq_lens`` [B] int32 counts each sequence's
+    cached tokens, these included: token t of q_len sees the first
+    seq_lens[b] - (q_len - 1 - t) of them.  Query head h reads key/value head
+    h // (q_heads / kv_heads).  ``sm_scale`` defaults to head_dim ** -0.5.
+    ``out`` is like ``q`` (dense); ``lse`` [B * q_len, q_heads] fp32 holds the
+    natural logarithm of each row's sum of exponentials.  A row that sees no key
+    gives zeros and -inf.  ``max_len``, the longest sequence's length, is a hint
+    for splitting the keys among blocks (0: the page table's capacity).
+    """
+    import torch
+    tp, stride, width, B = _page_table(page_table, cache)
+    if q.dim() != 3 or q.shape[1] % cache.kv_heads or q.shape[1] < 1:
+        raise ValueError("q must be [tokens, heads, head_dim] with a multiple of the cache's "
+                         "heads")
+    T, heads, dim = q.shape
+    qs = _token_stride(q, heads, cache.head_dim, "q", cache)
+    sp = _index_tensor(seq_lens, "seq_lens", cache, B)
+    if (T % B if B else T):
+        raise ValueError("q must hold the same number of tokens of each sequence")
+    q_len = T // B if B else 1
+    if q_len < 1:
+        raise ValueError("q must hold at least one token of each sequence")
+    with _allocating_on(stream, cache.device):
+        if out is None:
+            out = torch.empty((T, heads, dim), dtype=q.dtype, device=cache.device)
+        if lse is None and return_lse:
+            lse = torch.empty((T, heads), dtype=torch.float32, device=cache.device)
+        nbytes = pqg_kv_attention_workspace(cache.struct, width, B, q_len, heads, max_len)
+        if nbytes < 0:
+            raise PqgError(nbytes, "pqg_kv_attention_workspace")
+        work = torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
+    if (tuple(out.shape) != (T, heads, dim) or out.dtype != q.dtype or out.device != cache.device
+            or not out.is_contiguous()):
+        raise ValueError(f"out must be a contiguous {q.dtype} tensor {(T, heads, dim)} on the "
+                         f"cache's device")
+    if lse is not None and (tuple(lse.shape) != (T, heads) or lse.dtype != torch.float32
+                            or lse.device != cache.device or not lse.is_contiguous()):
+        raise ValueError(f"lse must be a contiguous fp32 tensor {(T, heads)} on the cache's device")
+    if stream is None:
+        stream = torch.cuda.current_stream(cache.device)
+    st = _on_device(cache.device, pqg_kv_attention, cache.struct, q.data_ptr(), qs, tp, stride,
+                    width, sp, B, q_len, heads,
+                    cache.head_dim ** -0.5 if sm_scale is None else float(sm_scale), max_len,
+                    out.data_ptr(), None if lse is None else lse.data_ptr(),
+                    None if work is None else work.data_ptr(), nbytes,
+                    PQG_BF16 if q.dtype == torch.bfloat16 else PQG_FP16,
+                    getattr(stream, "cuda_stream", stream))
+    if st != PQG_OK:
+        raise PqgError(st, "pqg_kv_attention")
+    return out if lse is None else (out, lse)

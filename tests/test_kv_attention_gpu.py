@@ -1,0 +1,293 @@
+"""Attention over the paged 4-bit cache against attention in 64 bits over the
+values the cache holds.
+
+Tolerances, for a row with weights p_j (their sum is 1) over L keys: the score
+of key j is off by at most e_j = (D + 8) 2^-24 sm_scale sum_d |q_d K_jd| (D
+products and sums in fp32, then a few factors) in natural units, with e = max_j
+e_j; a weight is rounded to 11 bits (2^-11 relative), its exponential is off by
+2^-21, and the sums over L keys lose at most L 2^-24 each.  So out is off by at
+most (2^-11 + 2^-20 + 2 e + 2 L 2^-24) sum_j p_j |V_j|, plus half a step of its
+type; lse by e + L 2^-24 + 2^-21 + 2^-22 |lse|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import cache_reference as ref
+from precision_activation_quantization_b200 import pqg
+
+pytestmark = pytest.mark.gpu
+
+G_SCALE = (84.0, 42.0)
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+E2M1 = torch.tensor(ref.E2M1)
+
+
+def build(lens, P, H, D, fmt, seed=0, spread=(118, 127), table_pad=2, extra=3):
+    """A cache whose used slots hold random codes and scales, with every other
+    slot (also the rest of a last page) at the largest code and a scale byte of
+    0xFF, which is no number; and its page table."""
+    rng = np.random.default_rng(seed)
+    used = [-(-n // P) for n in lens]
+    pages = sum(used) + extra
+    width = max(1, max(used, default=1)) + table_pad
+    table = np.full((len(lens), width), -1, np.int32)
+    order = rng.permutation(pages)[:sum(used)]
+    live = np.zeros((pages, P), bool)
+    for b, n in enumerate(used):
+        table[b, :n] = order[sum(used[:b]):sum(used[:b + 1])]
+        for i in range(n):
+            live[table[b, i], :min(P, lens[b] - i * P)] = True
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    live = torch.from_numpy(live).cuda()
+    args = []
+    for _ in range(2):
+        codes = torch.randint(0, 256, (pages, H, P, D // 2), generator=g, device="cuda", dtype=torch.uint8)
+        args.append(torch.where(live[:, None, :, None], codes, 0x77).contiguous())
+    lo, hi = spread if fmt == "mxfp4" else (24, 100)      # E4M3 2^-4 .. 24 over g
+    for _ in range(2):
+        sc = torch.randint(lo, hi, (pages, H, D // ref.GROUP[fmt], P), generator=g, device="cuda", dtype=torch.uint8)
+        args.append(torch.where(live[:, None, None, :], sc, 0xFF).contiguous())
+    gs = torch.tensor(G_SCALE, device="cuda") if fmt == "nvfp4" else None
+    return pqg.kv_cache(*args, fmt=fmt, global_scale=gs), torch.from_numpy(table).cuda()
+
+
+def values(codes, scales, fmt, g):
+    """float64 [.., P, D] of codes [.., P, D/2] and scales [.., D/G, P]."""
+    t = E2M1.to(codes.device)
+    v = torch.stack((t[(codes & 15).long()], t[(codes >> 4).long()]), -1).flatten(-2)
+    s = scales.transpose(-1, -2)
+    s = torch.exp2(s.double() - 127) if fmt == "mxfp4" else s.view(torch.float8_e4m3fn).double() / float(np.float32(g))
+    return v * s.repeat_interleave(ref.GROUP[fmt], -1)
+
+
+def reference(q, c, table, lens, q_len, sm_scale):
+    """(out, lse, weighted |V|, score error bound) in float64."""
+    T, Hq, D = q.shape
+    H, P = c.kv_heads, c.page_size
+    out = torch.zeros(T, Hq, D, dtype=torch.float64, device="cuda")
+    absv, lse = torch.zeros_like(out), torch.full((T, Hq), -torch.inf, dtype=torch.float64, device="cuda")
+    err = torch.zeros(T, Hq, dtype=torch.float64, device="cuda")
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        pages = table[b, :-(-n // P)].long()
+        good = ((pages >= 0) & (pages < c.num_pages)).repeat_interleave(P)[:n]
+        pg = pages.clamp(0, c.num_pages - 1)
+        k, v = (values(x[pg], s[pg], c.fmt, g).transpose(0, 1).flatten(1, 2)[:, :n] for x, s, g in
+                ((c.k_codes, c.k_scales, G_SCALE[0]), (c.v_codes, c.v_scales, G_SCALE[1])))
+        for t in range(q_len):
+            seen = good & (torch.arange(n, device="cuda") < n - (q_len - 1 - t))
+            if not bool(seen.any()):
+                continue
+            x = q[b * q_len + t].double().view(H, Hq // H, D)
+            kk, vv = k[:, seen], v[:, seen]
+            s = x @ kk.transpose(1, 2) * sm_scale
+            l = torch.logsumexp(s, -1)
+            p = (s - l[..., None]).exp()
+            i = b * q_len + t
+            out[i], lse[i] = (p @ vv).flatten(0, 1), l.flatten()
+            absv[i] = (p @ vv.abs()).flatten(0, 1)
+            err[i] = (x.abs() @ kk.abs().transpose(1, 2)).amax(-1).flatten() * abs(sm_scale) * (D + 8) * 2.0 ** -24
+    return out, lse, absv, err
+
+
+def compare(got, lse, want, in_dtype, lens, what=""):
+    out, wl, absv, err = want
+    L = max(list(lens) + [1])
+    half = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}[in_dtype]
+    tol = (2.0 ** -11 + 2.0 ** -20 + 2 * err[..., None] + 2 * L * 2.0 ** -24) * absv
+    tol = tol + half * (out.abs() + tol) + 2.0 ** -25
+    d = (got.double() - out).abs()
+    assert torch.isfinite(got).all(), what
+    assert (d <= tol).all(), f"{what}: {int((d > tol).sum())} off, worst {float((d / tol).max()):.2f} of the bound"
+    empty = torch.isinf(wl)
+    assert torch.equal(torch.isinf(lse) & (lse < 0), empty), what
+    assert (got[empty] == 0).all(), what
+    e = (lse.double() - wl)[~empty].abs()
+    assert (e <= (err + L * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -22 * wl.abs())[~empty]).all(), what
+
+
+def check(lens, q_len, Hq, H, D, P, fmt, in_dtype, seed=0, sm_scale=None, max_len=0, strided=False,
+          spread=(118, 127), q_size=1.0, table_pad=2):
+    c, table = build(lens, P, H, D, fmt, seed, spread, table_pad)
+    g = torch.Generator(device="cuda").manual_seed(seed + 1)
+    T = len(lens) * q_len
+    wide = torch.randn(T, (Hq + 2 * H) * D, generator=g, device="cuda").mul_(q_size).to(DT[in_dtype])
+    q = wide[:, :Hq * D].unflatten(1, (Hq, D))
+    q = q if strided else q.contiguous()
+    sm_scale = D ** -0.5 if sm_scale is None else sm_scale
+    out = torch.full((T + 1, Hq, D), 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full((T + 1, Hq), 7.0, device="cuda")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    pqg.kv_attention(q, c, table, n, sm_scale=sm_scale, max_len=max_len, out=out[:T], lse=lse[:T])
+    torch.cuda.synchronize()
+    assert (out[T:] == 7).all() and (lse[T:] == 7).all()
+    compare(out[:T], lse[:T], reference(q, c, table, lens, q_len, sm_scale), in_dtype, lens,
+            f"{lens} q_len {q_len} heads {Hq}/{H} D {D} P {P} {fmt} {in_dtype}")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("in_dtype", ["bf16", "fp16"])
+def test_types_and_head_dims(D, fmt, in_dtype):
+    check([1], 1, 4, 1, D, 16, fmt, in_dtype)
+    check([70, 0, 33, 16, 1], 1, 8, 2, D, 16, fmt, in_dtype, seed=1)
+    check([300, 517], 1, 12, 3, D, 64, fmt, in_dtype, seed=2, strided=True)
+
+
+@pytest.mark.parametrize("group", [1, 2, 3, 5, 7, 8, 9, 12, 16, 33])
+def test_head_groups(group):
+    check([65, 130], 1, 2 * group, 2, 128, 32, "mxfp4", "bf16", seed=group)
+    check([40], 2, group, 1, 64, 16, "nvfp4", "bf16", seed=group)
+
+
+@pytest.mark.parametrize("P", [16, 32, 64, 128, 256])
+def test_every_tail(P):
+    """Lengths around the edges of tiles and pages."""
+    for lens in ([15, 16, 17, 31, 32, 33], [47, 48, 49, 63, 64, 65, 127, 128, 129], [255, 256, 257, 511, 513]):
+        check(lens, 1, 8, 2, 64, P, "mxfp4", "bf16", seed=P)
+        check(lens, 1, 4, 1, 128, P, "nvfp4", "fp16", seed=P + 1)
+
+
+@pytest.mark.parametrize("q_len", [2, 3, 4, 7, 16])
+def test_several_tokens(q_len):
+    """Also sequences shorter than their new tokens: the first rows see no key."""
+    check([100, 1, 0, 33, q_len - 1, q_len, 600], q_len, 8, 2, 128, 32, "nvfp4", "bf16", seed=q_len)
+    check([64, 2], q_len, 5, 5, 64, 16, "mxfp4", "fp16", seed=q_len)
+
+
+def test_long_sequences_are_split_and_joined():
+    check([20000], 1, 8, 1, 128, 64, "mxfp4", "bf16")
+    check([9000, 40, 5000, 0, 12345], 1, 16, 4, 128, 64, "nvfp4", "fp16", seed=1)
+    check([7000], 3, 40, 2, 64, 16, "mxfp4", "bf16", seed=2)
+    check([5000], 1, 3, 1, 256, 128, "nvfp4", "bf16", seed=3)
+
+
+@pytest.mark.parametrize("max_len", [1, 100, 1000, 5000, 1 << 20])
+def test_the_length_hint_changes_nothing_but_the_split(max_len):
+    check([3000, 17, 999], 1, 8, 2, 128, 16, "mxfp4", "bf16", seed=3, max_len=max_len, table_pad=400)
+
+
+def test_sharp_and_flat_softmax():
+    check([700, 90], 1, 8, 2, 128, 32, "mxfp4", "bf16", q_size=40.0)          # one key takes all
+    check([700, 90], 1, 8, 2, 128, 32, "nvfp4", "fp16", q_size=0.0)           # all keys alike
+    check([700], 1, 8, 2, 128, 32, "nvfp4", "bf16", sm_scale=-0.3, seed=1)
+    check([700], 1, 8, 2, 128, 32, "mxfp4", "bf16", sm_scale=0.0, seed=1)
+
+
+def test_scales_far_apart():
+    """Groups whose scales span 2^40, and queries far from one in size."""
+    check([400, 31], 1, 8, 2, 128, 16, "mxfp4", "bf16", spread=(90, 131), sm_scale=1e-2)
+    check([400, 31], 2, 8, 2, 64, 16, "mxfp4", "fp16", spread=(96, 128), sm_scale=1e-2)
+    check([200], 1, 4, 1, 128, 16, "mxfp4", "bf16", spread=(20, 30), sm_scale=1.0, q_size=2.0 ** 90)
+    check([200], 1, 4, 1, 64, 16, "mxfp4", "bf16", spread=(200, 206), sm_scale=1.0, q_size=2.0 ** -80)
+    check([200], 1, 4, 1, 128, 16, "mxfp4", "fp16", spread=(118, 127), q_size=20000.0, sm_scale=1e-6)
+
+
+def test_bad_pages_are_not_seen():
+    lens, P = [100, 64, 40], 16
+    c, table = build(lens, P, 2, 64, "mxfp4")
+    table[0, 2], table[1, 0], table[2, :] = -5, c.num_pages, 2 ** 30
+    q = torch.randn(3, 4, 64, device="cuda", dtype=torch.bfloat16)
+    out, lse = pqg.kv_attention(q, c, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), return_lse=True)
+    compare(out, lse, reference(q, c, table, lens, 1, 64 ** -0.5), "bf16", lens)
+    assert (out[2] == 0).all()
+
+
+def test_lengths_outside_the_table_are_clamped():
+    c, table = build([48, 48], 16, 1, 64, "nvfp4", table_pad=0)
+    q = torch.randn(2, 2, 64, device="cuda", dtype=torch.float16)
+    out, lse = pqg.kv_attention(q, c, table, torch.tensor([2 ** 31 - 1, -3], dtype=torch.int32, device="cuda"), return_lse=True)
+    compare(out, lse, reference(q, c, table, [48, 0], 1, 64 ** -0.5), "fp16", [48])
+
+
+def test_masked_queries_are_not_read_into_others():
+    """A row that sees nothing, of infinities and not-numbers, leaves the others alone."""
+    lens = [2, 300]
+    c, table = build(lens, 32, 2, 128, "mxfp4")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(2 * 4, 6, 128, device="cuda", dtype=torch.bfloat16)
+    want = pqg.kv_attention(q, c, table, n)
+    q2 = q.clone()
+    q2[0], q2[1] = torch.inf, torch.nan           # tokens 0 and 1 of the first sequence see no key
+    got = pqg.kv_attention(q2, c, table, n)
+    assert (got[:2] == 0).all() and torch.equal(got[2:], want[2:])
+
+
+def test_deterministic_other_stream_graph_and_two_at_once():
+    lens = [5000, 300, 2500]
+    c, table = build(lens, 64, 4, 128, "nvfp4")
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = [torch.randn(3, 16, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    want = [pqg.kv_attention(x, c, table, n) for x in q]
+    side = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    for _ in range(10):                           # two calls in flight, each with its own scratch
+        got = [pqg.kv_attention(x, c, table, n, stream=s) for x, s in zip(q, side)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graphs = [torch.cuda.CUDAGraph() for _ in q]
+    outs = []
+    for x, g in zip(q, graphs):
+        with torch.cuda.graph(g):
+            outs.append(pqg.kv_attention(x, c, table, n))
+    for _ in range(5):
+        for g, s in zip(graphs, side):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    # lengths are read when the graph runs
+    n.copy_(torch.tensor([70, 0, 1], dtype=torch.int32))
+    graphs[0].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], pqg.kv_attention(q[0], c, table, n))
+    prev = pqg.pqg_set_pdl(False)
+    try:
+        assert torch.equal(outs[0], pqg.kv_attention(q[0], c, table, n))
+    finally:
+        pqg.pqg_set_pdl(prev)
+
+
+def test_a_cache_past_4_gb():
+    P, H, D = 256, 8, 256
+    pages = (5 << 30) // (P * H * D // 2)
+    big = pqg.kv_allocate(pages, P, H, D, fmt="mxfp4")
+    c, table = build([300, 511], P, H, D, "mxfp4", table_pad=0, extra=0)
+    far = torch.tensor([pages - 1, pages - 2, 2 ** 32 // (P * H * D // 2) + 1, 7], device="cuda")
+    for name in ("k_codes", "v_codes", "k_scales", "v_scales"):
+        getattr(big, name)[far] = getattr(c, name)
+    n = torch.tensor([300, 511], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 16, D, device="cuda", dtype=torch.bfloat16)
+    got = pqg.kv_attention(q, big, far[table.long()].to(torch.int32), n)
+    assert torch.equal(got, pqg.kv_attention(q, c, table, n))
+
+
+def test_nothing_to_do():
+    c, _ = build([5], 16, 1, 64, "mxfp4")
+    before = pqg.pqg_launch_count()
+    out = pqg.kv_attention(torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda"), c,
+                           torch.zeros(0, 4, dtype=torch.int32, device="cuda"),
+                           torch.zeros(0, dtype=torch.int32, device="cuda"))
+    assert out.shape == (0, 2, 64) and pqg.pqg_launch_count() == before
+
+
+def test_refusals():
+    c, table = build([40, 20], 16, 2, 64, "mxfp4")
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda")
+    n = torch.tensor([40, 20], dtype=torch.int32, device="cuda")
+    bad = [dict(q=q.float()), dict(q=q[:, :3]), dict(q=q[..., :32]), dict(q=q[0]), dict(q=q.cpu()),
+           dict(q=torch.zeros(3, 4, 64, dtype=q.dtype, device="cuda")), dict(q=q[:0]),
+           dict(seq_lens=n.long()), dict(seq_lens=n[:1]), dict(page_table=table.long()),
+           dict(page_table=table[0]), dict(sm_scale=float("inf")), dict(sm_scale=float("nan")),
+           dict(out=q.half()), dict(out=q[:1]), dict(lse=torch.zeros(2, 4, device="cuda").half()),
+           dict(lse=torch.zeros(4, 2, device="cuda")), dict(out=q), dict(q=q.transpose(0, 1).contiguous().transpose(0, 1)),
+           dict(q=torch.zeros(2 * 260 + 8, dtype=q.dtype, device="cuda")[4:].as_strided((2, 4, 64), (260, 64, 1)))]
+    for kw in bad:
+        args = dict(q=q, cache=c, page_table=table, seq_lens=n)
+        args.update(kw)
+        before = pqg.pqg_launch_count()
+        with pytest.raises((ValueError, TypeError, pqg.PqgError)):
+            pqg.kv_attention(**args)
+        assert pqg.pqg_launch_count() == before
