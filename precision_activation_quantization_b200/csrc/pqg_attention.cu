@@ -14,10 +14,11 @@ namespace {
 
 // How a call is cut: row tiles per key/value head, keys per chunk, chunks.
 struct Plan {
-    int64_t rows, row_tiles, chunk, chunks, workspace;
+    int64_t rows, n_tiles, row_tiles, chunk, chunks, workspace;
 };
 
-constexpr int64_t kMinChunk = 256;
+constexpr int64_t kBlockKeys = kAttentionWarps * kTileKeys;   // one tile per warp
+constexpr int64_t kMinChunk = 2 * kBlockKeys;
 constexpr int64_t kTargetBlocks = 148 * 16;
 
 int make_plan(const CacheView &c, int64_t max_pages, int64_t B, int64_t q_len, int64_t q_heads,
@@ -29,12 +30,14 @@ int make_plan(const CacheView &c, int64_t max_pages, int64_t B, int64_t q_len, i
     const int64_t cap = std::min<int64_t>(max_pages << c.page_shift, INT32_MAX);
     const int64_t len = max_len > 0 && max_len < cap ? max_len : cap;
     plan->rows = q_len * (q_heads / c.heads);
-    plan->row_tiles = (plan->rows + kAttentionThreads / 32 - 1) / (kAttentionThreads / 32);
+    // 16 rows to a block where there are more than 8 (not for a head of 256: registers)
+    plan->n_tiles = plan->rows > kTileRows && c.head_dim < 256 ? 2 : 1;
+    plan->row_tiles = (plan->rows + kTileRows * plan->n_tiles - 1) / (kTileRows * plan->n_tiles);
     const int64_t units = std::max<int64_t>(1, B * c.heads * plan->row_tiles);
     int64_t chunks = std::max<int64_t>(1, kTargetBlocks / units);
     chunks = std::min(chunks, (len + kMinChunk - 1) / kMinChunk);
     plan->chunk = (len + chunks - 1) / chunks;
-    plan->chunk = (plan->chunk + 31) / 32 * 32;
+    plan->chunk = (plan->chunk + kBlockKeys - 1) / kBlockKeys * kBlockKeys;
     plan->chunks = (len + plan->chunk - 1) / plan->chunk;
     if (units * plan->chunks >= (int64_t{1} << 31)) return PQG_ERR_INVALID_ARG;
     plan->workspace = 0;
@@ -47,8 +50,12 @@ template <typename In, int G, int D>
 cudaError_t launch_attention(const AttentionParams &p, const Plan &plan, cudaStream_t stream,
                              int *kernels) {
     const int64_t blocks = static_cast<int64_t>(p.B) * p.c.heads * plan.row_tiles * plan.chunks;
-    cudaError_t err =
-        launch(attention_kernel<In, G, D>, blocks, kAttentionThreads, 0, stream, p);
+    cudaError_t err;
+    if constexpr (D < 256)
+        err = launch(plan.n_tiles == 2 ? attention_kernel<In, G, D, 2> : attention_kernel<In, G, D, 1>,
+                     blocks, kAttentionThreads, 0, stream, p);
+    else
+        err = launch(attention_kernel<In, G, D, 1>, blocks, kAttentionThreads, 0, stream, p);
     *kernels = 1;
     if (err != cudaSuccess || plan.chunks == 1) return err;
     const int64_t joins = static_cast<int64_t>(p.B) * p.c.heads * p.rows;
