@@ -18,8 +18,14 @@ struct Plan {
 };
 
 constexpr int64_t kBlockKeys = kAttentionWarps * kTileKeys;   // one tile per warp
-constexpr int64_t kMinChunk = 2 * kBlockKeys;
-constexpr int64_t kTargetBlocks = 148 * 16;
+#ifndef PQG_ATT_MIN
+#define PQG_ATT_MIN 2
+#endif
+#ifndef PQG_ATT_BLOCKS
+#define PQG_ATT_BLOCKS 16
+#endif
+constexpr int64_t kMinChunk = PQG_ATT_MIN * kBlockKeys;
+constexpr int64_t kTargetBlocks = 148 * PQG_ATT_BLOCKS;
 
 int make_plan(const CacheView &c, int64_t max_pages, int64_t B, int64_t q_len, int64_t q_heads,
               int64_t max_len, Plan *plan) {
@@ -39,7 +45,9 @@ int make_plan(const CacheView &c, int64_t max_pages, int64_t B, int64_t q_len, i
     plan->chunk = (len + chunks - 1) / chunks;
     plan->chunk = (plan->chunk + kBlockKeys - 1) / kBlockKeys * kBlockKeys;
     plan->chunks = (len + plan->chunk - 1) / plan->chunk;
-    if (units * plan->chunks >= (int64_t{1} << 31)) return PQG_ERR_INVALID_ARG;
+    if (units * plan->chunks >= (int64_t{1} << 31) ||
+        B * c.heads * plan->rows >= (int64_t{1} << 31))
+        return PQG_ERR_INVALID_ARG;
     plan->workspace = 0;
     if (plan->chunks > 1)
         plan->workspace = B * c.heads * plan->chunks * plan->rows * (c.head_dim + 2) * 4;
@@ -61,8 +69,7 @@ cudaError_t launch_attention(const AttentionParams &p, const Plan &plan, cudaStr
     const int64_t joins = static_cast<int64_t>(p.B) * p.c.heads * p.rows;
     *kernels = 2;
     return launch(attention_join_kernel<In, G, D>,
-                  (joins + kAttentionThreads / 32 - 1) / (kAttentionThreads / 32),
-                  kAttentionThreads, 0, stream, p);
+                  joins, kAttentionThreads, 0, stream, p);
 }
 
 template <typename In, int G>

@@ -577,46 +577,71 @@ __global__ void __launch_bounds__(kAttentionThreads)
     release_dependents();
 }
 
-// Joins the chunks of one (sequence, query row): a warp per row.
+// Joins the chunks of one (sequence, query row): a block per row, whose warps
+// take every fourth chunk each.  The order of the sums is fixed.
 template <typename In, int G, int D>
 __global__ void __launch_bounds__(kAttentionThreads)
     attention_join_kernel(const __grid_constant__ AttentionParams p) {
-    constexpr int E = D / 32;
+    constexpr int E = D / 32;                  // elements a lane sums
+    __shared__ float sums[kAttentionWarps][D];
     wait_for_producer();
-    const uint32_t lane = threadIdx.x & 31u;
-    const uint64_t unit =
-        static_cast<uint64_t>(blockIdx.x) * (kAttentionThreads / 32) + (threadIdx.x >> 5);
-    const uint64_t bh = unit / p.rows;
-    const uint32_t r = static_cast<uint32_t>(unit - bh * p.rows);
-    const uint64_t b = bh / p.c.heads;
-    const uint32_t head = static_cast<uint32_t>(bh - b * p.c.heads);
-    if (b < p.B) {
-        const uint32_t used = used_chunks(p, sequence_length(p, static_cast<uint32_t>(b)));
-        if (used > 1u) {
-            const uint32_t t = r / p.group, qh = head * p.group + (r - t * p.group);
-            const uint64_t row = (b * p.q_len + t) * p.c.heads * p.group + qh;
-            const float inv_v = G == 16 ? __frcp_rn(__ldg(p.c.gscale + 1)) : 1.0f;
-            float m = kNoMax, l = 0.0f, acc[E];
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t r = blockIdx.x % p.rows, bh = blockIdx.x / p.rows;
+    const uint32_t head = bh % p.c.heads, b = bh / p.c.heads;
+    const uint32_t used = used_chunks(p, sequence_length(p, b));
+    if (used > 1u) {
+        const uint64_t slot = static_cast<uint64_t>(bh) * p.chunks * p.rows + r;
+        float m = kNoMax, l = 0.0f, acc[E];
 #pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-            for (uint32_t c = 0; c < used; ++c) m = fmaxf(m, p.stat[(bh * p.chunks + c) * p.rows + r].x);
-            for (uint32_t c = 0; c < used; ++c) {
-                const uint64_t slot = (bh * p.chunks + c) * p.rows + r;
-                const float2 st = p.stat[slot];
-                const float f = exp2f(st.x - m);
+        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+        for (uint32_t c = lane; c < used; c += 32u)
+            m = fmaxf(m, p.stat[slot + static_cast<uint64_t>(c) * p.rows].x);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        // 32 chunks at a time: a lane holds one chunk's factor, and every warp
+        // adds the values of 8 of them
+        for (uint32_t c0 = 0; c0 < used; c0 += 32u) {
+            float f = 0.0f;
+            if (c0 + lane < used) {
+                const float2 st = p.stat[slot + static_cast<uint64_t>(c0 + lane) * p.rows];
+                f = ex2_approx(st.x - m);
                 l = fmaf(st.y, f, l);
-#pragma unroll
-                for (int i = 0; i < E; ++i) acc[i] = fmaf(p.part[slot * D + lane * E + i], f, acc[i]);
             }
-            const float norm = l > 0.0f ? inv_v / l : 0.0f;
-            uint8_t *dst = p.out + (row * D + lane * E) * 2u;
 #pragma unroll
-            for (int i = 0; i < E; i += 2)
-                *reinterpret_cast<uint32_t *>(dst + 2 * i) =
-                    narrow2<In>(acc[i] * norm, acc[i + 1] * norm);
-            if (lane == 0 && p.lse != nullptr)
-                p.lse[row] = l > 0.0f ? (m - 7.0f + log2f(l)) * kLn2 : -INFINITY;
+            for (uint32_t i = 0; i < 32u / kAttentionWarps; ++i) {
+                const uint32_t c = c0 + i * kAttentionWarps + warp;
+                const float fc = __shfl_sync(0xFFFFFFFFu, f, i * kAttentionWarps + warp);
+                if (c < used) {                // warp-uniform
+                    uint32_t v[E];
+                    load_words(reinterpret_cast<const uint8_t *>(
+                                   p.part + (slot + static_cast<uint64_t>(c) * p.rows) * D + lane * E),
+                               v);
+#pragma unroll
+                    for (int k = 0; k < E; ++k) acc[k] = fmaf(__uint_as_float(v[k]), fc, acc[k]);
+                }
+            }
         }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+#pragma unroll
+        for (int k = 0; k < E; ++k) sums[warp][lane * E + k] = acc[k];
+        __syncthreads();
+        const float inv_v = G == 16 ? __frcp_rn(__ldg(p.c.gscale + 1)) : 1.0f;
+        const float norm = l > 0.0f ? inv_v / l : 0.0f;
+        const uint32_t t = r / p.group, qh = head * p.group + (r - t * p.group);
+        const uint64_t row = (static_cast<uint64_t>(b) * p.q_len + t) * p.c.heads * p.group + qh;
+        for (uint32_t d = 2u * threadIdx.x; d < D; d += 2u * kAttentionThreads) {
+            float x = 0.0f, y = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kAttentionWarps; ++w) {
+                x += sums[w][d];
+                y += sums[w][d + 1];
+            }
+            *reinterpret_cast<uint32_t *>(p.out + (row * D + d) * 2u) =
+                narrow2<In>(x * norm, y * norm);
+        }
+        if (threadIdx.x == 0u && p.lse != nullptr)
+            p.lse[row] = l > 0.0f ? (m - 7.0f + log2f(l)) * kLn2 : -INFINITY;
     }
     release_dependents();
 }
