@@ -17,7 +17,7 @@ struct Plan {
     int64_t rows, n_tiles, row_tiles, chunk, chunks, workspace;
 };
 
-constexpr int64_t kBlockKeys = kAttentionWarps * kTileKeys;   // one tile per warp
+constexpr int64_t kBlockKeys = 4 * kTileKeys;   // one or two tiles per warp
 #ifndef PQG_ATT_MIN
 #define PQG_ATT_MIN 2
 #endif
@@ -61,15 +61,15 @@ cudaError_t launch_attention(const AttentionParams &p, const Plan &plan, cudaStr
     cudaError_t err;
     if constexpr (D < 256)
         err = launch(plan.n_tiles == 2 ? attention_kernel<In, G, D, 2> : attention_kernel<In, G, D, 1>,
-                     blocks, kAttentionThreads, 0, stream, p);
+                     blocks, attention_warps(D) * 32, 0, stream, p);
     else
-        err = launch(attention_kernel<In, G, D, 1>, blocks, kAttentionThreads, 0, stream, p);
+        err = launch(attention_kernel<In, G, D, 1>, blocks, attention_warps(D) * 32, 0, stream, p);
     *kernels = 1;
     if (err != cudaSuccess || plan.chunks == 1) return err;
     const int64_t joins = static_cast<int64_t>(p.B) * p.c.heads * p.rows;
     *kernels = 2;
     return launch(attention_join_kernel<In, G, D>,
-                  joins, kAttentionThreads, 0, stream, p);
+                  joins, kJoinThreads, 0, stream, p);
 }
 
 template <typename In, int G>

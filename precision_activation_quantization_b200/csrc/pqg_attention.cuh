@@ -51,8 +51,8 @@ __device__ __forceinline__ uint32_t used_chunks(const AttentionParams &p, uint32
     return min((n + p.chunk - 1u) / p.chunk, p.chunks);
 }
 
-constexpr int kAttentionWarps = 4;
-constexpr int kAttentionThreads = kAttentionWarps * 32;
+// Warps of a block (a head of 256 takes more shared memory per warp).
+__host__ __device__ constexpr int attention_warps(int D) { return D < 256 ? 4 : 2; }
 constexpr int kTileKeys = 32;      // keys a warp takes at a time
 constexpr int kTileRows = 8;       // query rows of one matrix product (its N)
 
@@ -116,6 +116,36 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
     }
 }
 
+// N consecutive words of shared memory.
+template <int N>
+__device__ __forceinline__ void load_shared(const uint8_t *p, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+        }
+    }
+}
+
+// 16 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void commit_copies() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// All but the newest N groups of this thread's copies have landed.
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The largest of the four bytes of each word.
 template <int N>
 __device__ __forceinline__ uint32_t max_byte(const uint32_t (&w)[N]) {
@@ -164,27 +194,70 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // product wants pairs of keys in a register while the cache holds pairs of
 // elements: two words of two keys are interleaved by nibbles, two operations for
 // eight pairs.  The weights change from the first product's layout to the
-// second's by an 8 x 8 transpose.  No shared memory until the warps of a block
-// join: loads go to registers, those of the next tile are issued as soon as this
-// tile's registers are free.
+// second's by an 8 x 8 transpose.
+//
+// Every warp copies its own tiles into its own two buffers of shared memory
+// (asynchronous 16-byte copies, the next tile's in flight while one is computed),
+// so warps never wait on one another before the join.  A tile's rows are laid out
+// so that the lanes of one load meet 32 different banks (row_at below).
 //
 // The running maximum moves only when a score exceeds it by 2^8 (binary16 has
 // the room), so most tiles neither reduce it across lanes nor rescale.
 
 // A row of the first product's M, i.e. a lane's token of the tile:
 //   m-tile mt, rows gid and gid + 8  ->  tokens 4 gid + 2 mt and 4 gid + 2 mt + 1.
+// Where 16-byte part c of token r's codes lies in a tile of keys (values).
+// Lanes of one load differ in r / 4 (keys, read by gid) or r / 8 (values, read by
+// tig); those bits choose among the places of equal banks.
+template <int D>
+__device__ __forceinline__ uint32_t row_at(bool values, uint32_t r, uint32_t c) {
+    const uint32_t g = values ? r >> 3 : r >> 2;
+    if constexpr (D == 64)        // 4 rows of 2 parts per 128 bytes
+        return (r & ~3u) * 32u + ((r ^ g) & 3u) * 32u + c * 16u;
+    else if constexpr (D == 128)  // 2 rows of 4 parts
+        return (r & ~1u) * 64u + ((r ^ g) & 1u) * 64u + (values ? c ^ (g & 2u) : c) * 16u;
+    else                          // a row of 8 parts
+        return r * 128u + (values ? c ^ ((g << 1) & 6u) : c ^ (g & 1u)) * 16u;
+}
+
+template <int G, int D, int NT>
+struct AttentionShape {
+    static constexpr int kWarps = attention_warps(D);
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kRows = NT * kTileRows;            // query rows of the block
+    static constexpr int kCodes = kTileKeys * (D / 2);      // bytes of a tile's keys
+    static constexpr int kScales = kTileKeys * (D / G);
+    static constexpr int kTile = 2 * (kCodes + kScales);    // keys, values, their scales
+    static constexpr int kPad = D + 4;                      // floats of a row in the join
+    static constexpr int kJoin = kRows * kPad * 4;
+    static constexpr int kWarpBytes = 2 * kTile > kJoin ? 2 * kTile : kJoin;
+};
+
+// Blocks per SM the registers have to allow.
+#ifndef PQG_ATT_OCC
+#define PQG_ATT_OCC 4
+#endif
+#ifndef PQG_ATT_OCC2
+#define PQG_ATT_OCC2 2
+#endif
+template <int D, int NT>
+constexpr int attention_blocks() {
+    return D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? (NT == 1 ? PQG_ATT_OCC : PQG_ATT_OCC2) : 4;
+}
+
 template <typename In, int G, int D, int NT>
-__global__ void __launch_bounds__(kAttentionThreads)
+__global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, NT>())
     attention_kernel(const __grid_constant__ AttentionParams p) {
+    using Shape = AttentionShape<G, D, NT>;
+    constexpr int W = Shape::kWarps;
     constexpr int KW = D / 32;                 // words of a lane's part of a key
     constexpr int VW = D / 64;                 // words of a lane's part of a value
     constexpr int KG = D / 4 > G ? D / 4 / G : 1;   // groups a lane's part spans
     constexpr int VG = D / 8 > G ? D / 8 / G : 1;
     constexpr int MT = D / 16;                 // m-tiles of the second product
-    constexpr int R = NT * kTileRows;          // query rows of the block
-    constexpr int kPad = D + 4;
-    __shared__ float joined[kAttentionWarps][R][kPad];
-    __shared__ float stats[kAttentionWarps][R][2];
+    constexpr int R = Shape::kRows;
+    __shared__ __align__(128) uint8_t ring[W][Shape::kWarpBytes];
+    __shared__ float stats[W][R][2];
 
     wait_for_producer();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
@@ -267,87 +340,143 @@ __global__ void __launch_bounds__(kAttentionThreads)
     }
     uint32_t vref = 0u;                        // MXFP4: the values' reference exponent
 
-    // -- where a lane reads ------------------------------------------------------
+    // -- copying a tile -----------------------------------------------------------
     const uint32_t page_mask = (1u << p.c.page_shift) - 1u;
     const uint32_t code_page = (p.c.heads << p.c.page_shift) * (D / 2);
     const uint32_t scale_page = (p.c.heads << p.c.page_shift) * (D / G);
-    const uint32_t k_first = 4u * gid, v_first = 8u * tig;   // this lane's tokens of a tile
-    const uint8_t *k_code = p.c.codes[0] + (static_cast<uint64_t>(head) << p.c.page_shift) * (D / 2) +
-                            tig * (D / 8);
-    const uint8_t *v_code = p.c.codes[1] + (static_cast<uint64_t>(head) << p.c.page_shift) * (D / 2) +
-                            gid * (D / 16);
-    const uint8_t *k_scale = p.c.scales[0] + ((static_cast<uint64_t>(head) * (D / G) +
-                                               tig * (D / 4) / G) << p.c.page_shift);
-    const uint8_t *v_scale = p.c.scales[1] + ((static_cast<uint64_t>(head) * (D / G) +
-                                               gid * (D / 8) / G) << p.c.page_shift);
     const int32_t *table = p.table + static_cast<uint64_t>(b) * p.table_stride;
+    uint8_t *const mine = ring[warp];
+    const uint32_t mine_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+    // this lane's 16-byte part of the first rows, in the cache and in the tile; a
+    // copy takes kRowsPerCopy rows, and row_at's choice of place for later rows is
+    // that of row0 with a bit or two flipped
+    constexpr uint32_t kParts = D / 32, kRowsPerCopy = 32 / kParts;
+    const uint32_t row0 = lane / kParts, part = lane % kParts;
+    const uint32_t code_at = ((head << p.c.page_shift) + row0) * (D / 2) + part * 16u;
+    const uint32_t to_k = row_at<D>(false, row0, part), to_v = row_at<D>(true, row0, part);
+    // this lane's part of the scales: 16 tokens of one group, keys' groups first
+    constexpr uint32_t kScaleParts = 4u * (D / G);
+    const uint32_t scale_half = lane & 1u;
+    const uint8_t *scale_src[(kScaleParts + 31) / 32];
+#pragma unroll
+    for (uint32_t i = 0; i < kScaleParts; i += 32u) {
+        const uint32_t at = (i + lane) % kScaleParts, g = (at >> 1) % (D / G);
+        scale_src[i / 32u] = p.c.scales[at / (2u * (D / G))] +
+                             ((static_cast<uint64_t>(head) * (D / G) + g) << p.c.page_shift);
+    }
 
-    // pages of this lane's keys and of its values in the tile at j (-1: none)
-    auto pages = [&](uint32_t j, int &kp, int &vp) {
-        kp = vp = -1;
-        if (j + (k_first & 16u) < n) kp = __ldg(table + ((j + (k_first & 16u)) >> p.c.page_shift));
-        if (j + (v_first & 16u) < n) vp = __ldg(table + ((j + (v_first & 16u)) >> p.c.page_shift));
-        if (static_cast<uint32_t>(kp) >= p.c.num_pages) kp = -1;
-        if (static_cast<uint32_t>(vp) >= p.c.num_pages) vp = -1;
-    };
-    uint32_t kraw[4][KW], vraw[8][VW], ksc[KG], vsc[VG][2];
-    auto load_keys = [&](uint32_t j, int page) {
-        const uint64_t pg = static_cast<uint32_t>(max(page, 0));
-        const uint32_t off = (j + k_first) & page_mask;
-        const uint8_t *c = k_code + pg * code_page + off * (D / 2);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) load_words(c + x * (D / 2), kraw[x]);
-        const uint8_t *s = k_scale + pg * scale_page + off;
-#pragma unroll
-        for (int g = 0; g < KG; ++g) {
-            uint32_t w[1];
-            load_words(s + (g << p.c.page_shift), w);
-            ksc[g] = w[0];
+    // pages of the two halves of the tile at j (-1: none)
+    auto pages = [&](uint32_t j, int (&pg)[2]) {
+        pg[0] = __ldg(table + (j >> p.c.page_shift));
+        pg[1] = pg[0];
+        if (p.c.page_shift < 5u) {
+            pg[1] = -1;
+            if (j + 16u < n) pg[1] = __ldg(table + ((j + 16u) >> p.c.page_shift));
         }
     };
-    auto load_values = [&](uint32_t j, int page) {
-        const uint64_t pg = static_cast<uint32_t>(max(page, 0));
-        const uint32_t off = (j + v_first) & page_mask;
-        const uint8_t *c = v_code + pg * code_page + off * (D / 2);
+    auto copy_tile = [&](uint32_t j, int (&pg)[2], uint32_t buffer) {
+        const uint32_t to = mine_at + buffer * Shape::kTile;
+        const uint32_t off = j & page_mask, off1 = p.c.page_shift < 5u ? 0u : off + 16u;
 #pragma unroll
-        for (int x = 0; x < 8; ++x) load_words(c + x * (D / 2), vraw[x]);
-        const uint8_t *s = v_scale + pg * scale_page + off;
+        for (int h = 0; h < 2; ++h)
+            if (static_cast<uint32_t>(pg[h]) >= p.c.num_pages) pg[h] = -1;
 #pragma unroll
-        for (int g = 0; g < VG; ++g) load_words(s + (g << p.c.page_shift), vsc[g]);
+        for (int h = 0; h < 2; ++h) {          // 16 tokens lie in one page
+            const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(max(pg[h], 0))) *
+                                    code_page + (code_at + (h ? off1 : off) * (D / 2));
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const uint8_t *src = p.c.codes[x] + at;
+#pragma unroll
+                for (uint32_t r = 0; r < 16; r += kRowsPerCopy) {
+                    const uint32_t row = 16u * h + r;
+                    // the bits that row changes in row_at(row + row0) beyond its own place
+                    const uint32_t flip = row_at<D>(x == 1, row, 0) ^ (row * (D / 2));
+                    copy16(to + x * Shape::kCodes + row * (D / 2) + ((x ? to_v : to_k) ^ flip),
+                           src + r * (D / 2));
+                }
+            }
+        }
+        const uint64_t at = static_cast<uint64_t>(static_cast<uint32_t>(
+                                max(scale_half ? pg[1] : pg[0], 0))) * scale_page +
+                            (scale_half ? off1 : off);
+#pragma unroll
+        for (uint32_t i = 0; i < kScaleParts; i += 32u)
+            if (i + lane < kScaleParts)
+                copy16(to + 2 * Shape::kCodes + (i + lane) * 16u, scale_src[i / 32u] + at);
     };
 
-    // -- the warp's tiles: every 4th of the chunk, and of the chunks that wrap ----
+    // -- the warp's tiles: every W-th of the chunk, and of the chunks that wrap ---
     const uint64_t lap = static_cast<uint64_t>(p.chunk) * p.chunks;
     uint64_t first = static_cast<uint64_t>(chunk) * p.chunk;
     uint32_t in_chunk = warp * kTileKeys;
     auto next_tile = [&]() {                   // the tile after this one
-        in_chunk += kAttentionWarps * kTileKeys;
+        in_chunk += W * kTileKeys;
         if (in_chunk >= p.chunk) {
             in_chunk = warp * kTileKeys;
             first += lap;
         }
+        return first + in_chunk;
     };
-    uint64_t j64 = first + in_chunk;
-    int kp = -1, vp = -1, kp_next = -1, vp_next = -1;
-    bool more = in_chunk < p.chunk && j64 < n;
+    // pages are read a tile before the copies that need them
+    uint64_t j64 = first + in_chunk, next64 = 0;
+    int pg[2] = {-1, -1}, pg_next[2] = {-1, -1};
+    bool more = j64 < n;
     if (more) {
-        pages(static_cast<uint32_t>(j64), kp, vp);
-        load_keys(static_cast<uint32_t>(j64), kp);
-        load_values(static_cast<uint32_t>(j64), vp);
+        pages(static_cast<uint32_t>(j64), pg);
+        next64 = next_tile();
+        if (next64 < n) pages(static_cast<uint32_t>(next64), pg_next);
+        copy_tile(static_cast<uint32_t>(j64), pg, 0u);   // (a page outside the cache becomes -1)
     }
+    commit_copies();
+    const uint32_t k_first = 4u * gid, v_first = 8u * tig;   // this lane's tokens of a tile
+    // this lane's codes of its even and odd keys, and of its even and odd values (rows
+    // four, or two, apart lie that many rows apart: see the reads below)
+    const uint8_t *const scales_at = mine + 2 * Shape::kCodes;
+    const uint32_t k_scale_at = tig * (D / 4) / G * kTileKeys + k_first;
+    const uint32_t v_scale_at = Shape::kScales + gid * (D / 8) / G * kTileKeys + v_first;
+    constexpr uint32_t kCycle = D == 64 ? 4 : D == 128 ? 2 : 1;   // rows per 128 bytes
+    uint32_t k_at[kCycle], v_at[kCycle];
+#pragma unroll
+    for (uint32_t x = 0; x < kCycle; ++x) {
+        k_at[x] = row_at<D>(false, k_first + x, tig * (D / 8) / 16u) + (tig * (D / 8)) % 16u;
+        v_at[x] = Shape::kCodes + row_at<D>(true, v_first + x, gid * (D / 16) / 16u) +
+                  (gid * (D / 16)) % 16u;
+    }
+    uint32_t buffer = 0;
     while (more) {
         const uint32_t j = static_cast<uint32_t>(j64);
-        next_tile();
-        j64 = first + in_chunk;
+        const int now[2] = {pg[0], pg[1]};
+        // the other buffer's tile is done with (the loop ends in __syncwarp)
+        j64 = next64;
         more = j64 < n;
-        if (more) pages(static_cast<uint32_t>(j64), kp_next, vp_next);
+        pg[0] = pg_next[0];
+        pg[1] = pg_next[1];
+        if (more) {
+            copy_tile(static_cast<uint32_t>(j64), pg, buffer ^ 1u);
+            next64 = next_tile();
+            if (next64 < n) pages(static_cast<uint32_t>(next64), pg_next);
+        }
+        commit_copies();
+        wait_copies<1>();
+        __syncwarp();
+        const uint32_t tile_at = buffer * Shape::kTile;
+        uint32_t ksc[KG], vsc[VG][2];
+#pragma unroll
+        for (int g = 0; g < KG; ++g)
+            ksc[g] = *reinterpret_cast<const uint32_t *>(scales_at + tile_at + k_scale_at +
+                                                         g * kTileKeys);
+#pragma unroll
+        for (int g = 0; g < VG; ++g)
+            load_shared(scales_at + tile_at + v_scale_at + g * kTileKeys, vsc[g]);
 
         // a tile some of whose keys some row does not see (warp-uniform)
-        const bool edge = static_cast<int>(j + kTileKeys) > static_cast<int>(n - (p.q_len - 1u)) ||
-                          __any_sync(0xFFFFFFFFu, kp < 0);
+        const bool edge =
+            static_cast<int>(j + kTileKeys) > static_cast<int>(n - (p.q_len - 1u)) ||
+            now[0] < 0 || now[1] < 0;
         const int live = static_cast<int>(n - j);          // tokens of the tile in the sequence
-        const int k_end = kp < 0 ? 0 : live, v_end = vp < 0 ? 0 : live;
         if (edge) {                            // scales of keys that are not there may be anything
+            const int k_end = (gid < 4u ? now[0] : now[1]) < 0 ? 0 : live, v_end = (tig < 2u ? now[0] : now[1]) < 0 ? 0 : live;
 #pragma unroll
             for (int g = 0; g < KG; ++g) ksc[g] = keep_bytes(ksc[g], k_first, k_end);
 #pragma unroll
@@ -381,6 +510,20 @@ __global__ void __launch_bounds__(kAttentionThreads)
             // 2^(kref - 127 - 12); below 2^-126 the scores are nothing
             tile_scale = kref > 12u ? __uint_as_float((kref - 12u) << 23) : 0.0f;
         }
+        uint32_t kraw[4][KW];
+#pragma unroll
+        for (uint32_t x = 0; x < 4; ++x) {
+            const uint8_t *at = mine + tile_at + k_at[x % kCycle] + x / kCycle * 128u;
+            if constexpr (D == 256) {          // two 16-byte parts, which row_at may swap
+                uint32_t lo[4], hi[4];
+                load_shared(at, lo);
+                load_shared(mine + tile_at + (k_at[0] ^ 16u) + x * 128u, hi);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) kraw[x][i] = lo[i], kraw[x][i + 4] = hi[i];
+            } else {
+                load_shared(at, kraw[x]);
+            }
+        }
         float c[2][NT][4];
 #pragma unroll
         for (int mt = 0; mt < 2; ++mt)
@@ -408,7 +551,6 @@ __global__ void __launch_bounds__(kAttentionThreads)
                 }
             }
         }
-        if (more) load_keys(static_cast<uint32_t>(j64), kp_next);
 
         // -- weights ------------------------------------------------------------------
         uint32_t weights[NT][4];               // B operand: [2 * k-step + half]
@@ -425,7 +567,8 @@ __global__ void __launch_bounds__(kAttentionThreads)
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        if (kp < 0 || static_cast<int>(j + k_first + x) >= limit[nt][k])
+                        if ((gid < 4u ? now[0] : now[1]) < 0 ||
+                            static_cast<int>(j + k_first + x) >= limit[nt][k])
                             s[x][k] = -INFINITY;
             }
             float top[2];
@@ -493,6 +636,10 @@ __global__ void __launch_bounds__(kAttentionThreads)
                 vs[0][x] = relative_power2(
                     __byte_perm(vsc[0][0], vsc[0][1], (x + 4) << 8 | x) & 0x00FF00FFu, vref);
         }
+        uint32_t vraw[8][VW];
+#pragma unroll
+        for (uint32_t x = 0; x < 8; ++x)
+            load_shared(mine + tile_at + v_at[x % kCycle] + x / kCycle * 128u, vraw[x]);
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
 #pragma unroll
@@ -518,10 +665,11 @@ __global__ void __launch_bounds__(kAttentionThreads)
                                  weights[nt][2 * ks2], weights[nt][2 * ks2 + 1]);
             }
         }
-        if (more) load_values(static_cast<uint32_t>(j64), vp_next);
-        kp = kp_next;
-        vp = vp_next;
+        __syncwarp();
+        buffer ^= 1u;
     }
+    wait_copies<0>();
+    __syncwarp();                              // the buffers are free for the join
 
     // -- join the block's warps ----------------------------------------------------------
     const float unit = G == 16 ? 1.0f : exp2f(static_cast<float>(vref) - 139.0f);
@@ -538,22 +686,23 @@ __global__ void __launch_bounds__(kAttentionThreads)
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                *reinterpret_cast<float2 *>(&joined[warp][r][gid * (D / 8) + 2 * i]) =
+                *reinterpret_cast<float2 *>(mine + (r * Shape::kPad + gid * (D / 8) + 2 * i) * 4) =
                     make_float2(acc[i][nt][k] * unit, acc[i][nt][k + 2] * unit);
         }
     }
     __syncthreads();
     const float inv_v = G == 16 ? __frcp_rn(__ldg(p.c.gscale + 1)) : 1.0f;
-    for (uint32_t i = threadIdx.x; i < R * (D / 2); i += kAttentionThreads) {
+    for (uint32_t i = threadIdx.x; i < R * (D / 2); i += Shape::kThreads) {
         const uint32_t r = i / (D / 2), d = i % (D / 2) * 2u, row = tile * R + r;
         if (row >= p.rows) break;
         float top = kNoMax, sum = 0.0f, x = 0.0f, y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kAttentionWarps; ++w) top = fmaxf(top, stats[w][r][0]);
+        for (int w = 0; w < W; ++w) top = fmaxf(top, stats[w][r][0]);
 #pragma unroll
-        for (int w = 0; w < kAttentionWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             const float f = ex2_approx(stats[w][r][0] - top);
-            const float2 o = *reinterpret_cast<const float2 *>(&joined[w][r][d]);
+            const float2 o =
+                *reinterpret_cast<const float2 *>(ring[w] + (r * Shape::kPad + d) * 4);
             sum = fmaf(stats[w][r][1], f, sum);
             x = fmaf(o.x, f, x);
             y = fmaf(o.y, f, y);
@@ -577,13 +726,16 @@ __global__ void __launch_bounds__(kAttentionThreads)
     release_dependents();
 }
 
+constexpr int kJoinWarps = 4;
+constexpr int kJoinThreads = kJoinWarps * 32;
+
 // Joins the chunks of one (sequence, query row): a block per row, whose warps
 // take every fourth chunk each.  The order of the sums is fixed.
 template <typename In, int G, int D>
-__global__ void __launch_bounds__(kAttentionThreads)
+__global__ void __launch_bounds__(kJoinThreads)
     attention_join_kernel(const __grid_constant__ AttentionParams p) {
     constexpr int E = D / 32;                  // elements a lane sums
-    __shared__ float sums[kAttentionWarps][D];
+    __shared__ float sums[kJoinWarps][D];
     wait_for_producer();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t r = blockIdx.x % p.rows, bh = blockIdx.x / p.rows;
@@ -608,9 +760,9 @@ __global__ void __launch_bounds__(kAttentionThreads)
                 l = fmaf(st.y, f, l);
             }
 #pragma unroll
-            for (uint32_t i = 0; i < 32u / kAttentionWarps; ++i) {
-                const uint32_t c = c0 + i * kAttentionWarps + warp;
-                const float fc = __shfl_sync(0xFFFFFFFFu, f, i * kAttentionWarps + warp);
+            for (uint32_t i = 0; i < 32u / kJoinWarps; ++i) {
+                const uint32_t c = c0 + i * kJoinWarps + warp;
+                const float fc = __shfl_sync(0xFFFFFFFFu, f, i * kJoinWarps + warp);
                 if (c < used) {                // warp-uniform
                     uint32_t v[E];
                     load_words(reinterpret_cast<const uint8_t *>(
@@ -630,10 +782,10 @@ __global__ void __launch_bounds__(kAttentionThreads)
         const float norm = l > 0.0f ? inv_v / l : 0.0f;
         const uint32_t t = r / p.group, qh = head * p.group + (r - t * p.group);
         const uint64_t row = (static_cast<uint64_t>(b) * p.q_len + t) * p.c.heads * p.group + qh;
-        for (uint32_t d = 2u * threadIdx.x; d < D; d += 2u * kAttentionThreads) {
+        for (uint32_t d = 2u * threadIdx.x; d < D; d += 2u * kJoinThreads) {
             float x = 0.0f, y = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kAttentionWarps; ++w) {
+            for (int w = 0; w < kJoinWarps; ++w) {
                 x += sums[w][d];
                 y += sums[w][d + 1];
             }
