@@ -1,10 +1,11 @@
-"""Build libpqg.so in-tree with nvcc for sm_100a.
+"""Build libpqg.so in-tree with nvcc for sm_100a, and its tensor binding.
 
     python -m precision_activation_quantization_b200.build [--force] [--verbose]
 
 Each translation unit under csrc/ compiles in parallel to an object in _build/,
 and then everything links into precision_activation_quantization_b200/libpqg.so
-against the static CUDA runtime.  No fast-math: the codes and scales must be
+against the static CUDA runtime.  csrc/pqg_torch.cpp, which marshals torch tensors
+for the C ABI, becomes _pqg_torch.so beside it.  No fast-math: the codes and scales must be
 bit-exact, so every division and reciprocal has to round correctly.
 """
 from __future__ import annotations
@@ -14,6 +15,7 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -21,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpqg.so")
+BINDING = os.path.join(PKG, "_pqg_torch.so")
+BINDING_SRC = os.path.join(CSRC, "pqg_torch.cpp")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -85,12 +89,39 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: str = LIB
     return out
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile _pqg_torch.so against the installed torch unless it is newer than
+    its sources."""
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "pqg.h"), os.path.abspath(__file__)]
+    if (not force and os.path.exists(BINDING)
+            and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps)):
+        return BINDING
+    import torch
+    home = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    include = [os.path.join(home, "include"),
+               os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"], INCLUDE]
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}"]
+           + [f"-isystem{d}" for d in include] + ["-o", tmp, BINDING_SRC]
+           + ["-L" + os.path.join(home, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+              "-ltorch_cuda", "-ltorch_python", "-ldl"])
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--force", action="store_true")
     ap.add_argument("--verbose", action="store_true", help="print ptxas register/spill info")
     args = ap.parse_args()
     print(build(force=args.force, verbose=args.verbose))
+    print(build_binding(force=args.force))
 
 
 if __name__ == "__main__":

@@ -238,7 +238,7 @@ struct AttentionShape {
 #define PQG_ATT_OCC 4
 #endif
 #ifndef PQG_ATT_OCC2
-#define PQG_ATT_OCC2 2
+#define PQG_ATT_OCC2 3
 #endif
 template <int D, int NT>
 constexpr int attention_blocks() {
@@ -258,6 +258,9 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
     constexpr int R = Shape::kRows;
     __shared__ __align__(128) uint8_t ring[W][Shape::kWarpBytes];
     __shared__ float stats[W][R][2];
+    __shared__ uint2 queries[NT][MT][32];      // the first product's B operand, per lane
+    __shared__ float shrinks[R];
+    static_assert(NT <= W, "a warp prepares 8 query rows");
 
     wait_for_producer();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
@@ -273,56 +276,6 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
     if (chunk >= max(used, 1u)) {
         release_dependents();
         return;
-    }
-
-    // -- the query rows, normalised, as the first product's B operand -----------
-    uint32_t q[NT][MT][2];
-    float head_scale[NT][2];                   // of this lane's columns 2 tig, 2 tig + 1
-    int limit[NT][2];                          // keys they see
-    const float inv_k = G == 16 ? __frcp_rn(__ldg(p.c.gscale)) : 1.0f;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t r = tile * R + nt * kTileRows + gid;
-        uint32_t raw[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) raw[i] = 0u;
-        if (r < p.rows) {
-            const uint32_t t = r / p.group, qh = head * p.group + (r - t * p.group);
-            const uint64_t token = static_cast<uint64_t>(b) * p.q_len + t;
-            load_words(p.q + (token * p.q_stride + static_cast<uint64_t>(qh) * D + tig * (D / 4)) * 2u,
-                       raw);
-        }
-        float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            float lo, hi;
-            widen2<In>(raw[i], lo, hi);
-            top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        // 2^(14 - exponent), at most 2^126 (so that its reciprocal is normal)
-        const int e = static_cast<int>(__float_as_uint(top) >> 23);
-        const int up = min(max(268 - e, 14), 253);
-        const float grow = __uint_as_float(static_cast<uint32_t>(up) << 23);
-        const float shrink = __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float lo, hi;
-                widen2<In>(raw[2 * i + k], lo, hi);
-                q[nt][i][k] = narrow2<__half>(lo * grow, hi * grow);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t col = 2u * tig + k;
-            head_scale[nt][k] = __shfl_sync(0xFFFFFFFFu, shrink, col * 4u) * (p.scale_log2 * inv_k);
-            const uint32_t rc = tile * R + nt * kTileRows + col;
-            limit[nt][k] = static_cast<int>(n) - static_cast<int>(p.q_len - 1u) +
-                           static_cast<int>(min(rc / p.group, p.q_len - 1u));
-        }
     }
 
     float acc[MT][NT][4], m[NT][2], l[NT][2];
@@ -429,6 +382,58 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
         copy_tile(static_cast<uint32_t>(j64), pg, 0u);   // (a page outside the cache becomes -1)
     }
     commit_copies();
+    // -- the query rows, normalised: a warp each for 8 of them, while tiles come ---
+    if (warp < NT) {
+        const uint32_t r = tile * R + warp * kTileRows + gid;
+        uint32_t raw[D / 8];
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) raw[i] = 0u;
+        if (r < p.rows) {
+            const uint32_t t = r / p.group, qh = head * p.group + (r - t * p.group);
+            const uint64_t token = static_cast<uint64_t>(b) * p.q_len + t;
+            load_words(p.q + (token * p.q_stride + static_cast<uint64_t>(qh) * D + tig * (D / 4)) * 2u,
+                       raw);
+        }
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            float lo, hi;
+            widen2<In>(raw[i], lo, hi);
+            top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // 2^(14 - exponent), at most 2^126 (so that its reciprocal is normal)
+        const int e = static_cast<int>(__float_as_uint(top) >> 23);
+        const int up = min(max(268 - e, 14), 253);
+        const float grow = __uint_as_float(static_cast<uint32_t>(up) << 23);
+        if (tig == 0u)
+            shrinks[warp * kTileRows + gid] =
+                __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            float x0, x1, x2, x3;
+            widen2<In>(raw[2 * i], x0, x1);
+            widen2<In>(raw[2 * i + 1], x2, x3);
+            queries[warp][i][lane] = make_uint2(narrow2<__half>(x0 * grow, x1 * grow),
+                                                narrow2<__half>(x2 * grow, x3 * grow));
+        }
+    }
+    __syncthreads();
+    float head_scale[NT][2];                   // of this lane's columns 2 tig, 2 tig + 1
+    int limit[NT][2];                          // keys they see
+    const float inv_k = G == 16 ? __frcp_rn(__ldg(p.c.gscale)) : 1.0f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t col = nt * kTileRows + 2u * tig + k;
+            head_scale[nt][k] = shrinks[col] * (p.scale_log2 * inv_k);
+            limit[nt][k] = static_cast<int>(n) - static_cast<int>(p.q_len - 1u) +
+                           static_cast<int>(min((tile * R + col) / p.group, p.q_len - 1u));
+        }
+    }
+
     const uint32_t k_first = 4u * gid, v_first = 8u * tig;   // this lane's tokens of a tile
     // this lane's codes of its even and odd keys, and of its even and odd values (rows
     // four, or two, apart lie that many rows apart: see the reads below)
@@ -533,6 +538,12 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
                 for (int k = 0; k < 4; ++k) c[mt][nt][k] = 0.0f;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
+            uint2 q[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                q[nt][0] = queries[nt][2 * w][lane];
+                q[nt][1] = queries[nt][2 * w + 1][lane];
+            }
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
                 uint32_t a[4], a8[4];
@@ -545,9 +556,8 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
                 }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    mma16816(c[mt][nt], a[0], a8[0], a[1], a8[1], q[nt][2 * w][0], q[nt][2 * w][1]);
-                    mma16816(c[mt][nt], a[2], a8[2], a[3], a8[3], q[nt][2 * w + 1][0],
-                             q[nt][2 * w + 1][1]);
+                    mma16816(c[mt][nt], a[0], a8[0], a[1], a8[1], q[nt][0].x, q[nt][0].y);
+                    mma16816(c[mt][nt], a[2], a8[2], a[3], a8[3], q[nt][1].x, q[nt][1].y);
                 }
             }
         }

@@ -442,13 +442,33 @@ def _allocating_on(stream, device):
     return torch.cuda.stream(stream)
 
 
-def _on_device(device, function, *args):
-    """Call a C entry point with ``device`` current."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        return function(*args)
-    with torch.cuda.device(device):
-        return function(*args)
+_native = None
+
+
+def native():
+    """The tensor binding (csrc/pqg_torch.cpp), built first when it is missing or
+    older than its sources, calling the library this module loaded."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (its libraries resolve the binding's symbols)
+        _build.build_binding()
+        from . import _pqg_torch
+        _pqg_torch.load(LIBRARY_PATH)
+        _native = _pqg_torch
+    return _native
+
+
+def _call(function, stream, device, *args):
+    """A native entry point on ``stream`` (None: torch's current stream); returns
+    what it made, or raises on a non-OK status."""
+    if stream is None:
+        result = function(*args, None)
+    else:
+        with _allocating_on(stream, device):
+            result = function(*args, getattr(stream, "cuda_stream", stream))
+    if result[0] != PQG_OK:
+        raise PqgError(result[0], result[1])
+    return result[2:]
 
 
 def rmsnorm_quant(x, weight, residual=None, out=None, scales=None, *, residual_out=None,
@@ -467,62 +487,9 @@ def rmsnorm_quant(x, weight, residual=None, out=None, scales=None, *, residual_o
     rows.  NVFP4 is ``out_dtype="e2m1", scale_fmt="e4m3", group=16`` with
     ``global_scale``.  The call runs with ``x``'s device current.
     """
-    import torch
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"unsupported input dtype {x.dtype}")
-    if not x.is_cuda or not x.is_contiguous() or x.dim() < 2:
-        raise ValueError("x must be a contiguous CUDA tensor of rows")
-    K = x.shape[-1]
-    M = x.numel() // K if K else 0
-    dev = x.device
-    if (weight.dtype != x.dtype or weight.numel() != K or weight.device != dev
-            or not weight.is_contiguous()):
-        raise ValueError(f"weight must be a contiguous {x.dtype} tensor of {K} entries on "
-                         f"x's device")
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out needs a residual: without one h is x")
-    else:
-        if residual_out is None:
-            with _allocating_on(stream, dev):
-                residual_out = torch.empty_like(x)
-        for name, t in (("residual", residual), ("residual_out", residual_out)):
-            if (t.dtype != x.dtype or t.numel() != x.numel() or t.device != dev
-                    or not t.is_contiguous()):
-                raise ValueError(f"{name} must be a contiguous {x.dtype} tensor of x's size on "
-                                 f"its device")
-    if out is None or scales is None:
-        with _allocating_on(stream, dev):
-            o, sc = allocate_outputs(M, K, group, out_dtype=out_dtype, scale_fmt=scale_fmt,
-                                     layout=layout, device=dev)
-        out = o[0] if out is None else out
-        scales = sc[0] if scales is None else scales
-    out_bytes = M * (K // 2 if out_dtype == "e2m1" else K)
-    if out.numel() * out.element_size() != out_bytes or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous buffer of {out_bytes} bytes")
-    nbytes = pqg_scales_bytes(1, M, K, group, SCALE_FMTS[scale_fmt], LAYOUTS[layout])
-    if (nbytes >= 0 and scales.numel() * scales.element_size() != nbytes) \
-            or not scales.is_contiguous():
-        raise ValueError(f"scales must be a contiguous buffer of {nbytes} bytes")
-    if not (out.device == scales.device == dev):
-        raise ValueError("x, out and scales must be on the same CUDA device")
-    gptr = None
-    if scale_fmt == "e4m3":
-        if (global_scale is None or global_scale.dtype != torch.float32
-                or global_scale.numel() != 1 or global_scale.device != dev):
-            raise ValueError("NVFP4 needs global_scale: a one-element fp32 tensor on x's device")
-        gptr = global_scale.data_ptr()
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    st = _on_device(dev, pqg_rmsnorm_quant, x.data_ptr(),
-                    None if residual is None else residual.data_ptr(), weight.data_ptr(),
-                    None if residual is None else residual_out.data_ptr(), out.data_ptr(),
-                    scales.data_ptr(), gptr, M, K, group, float(eps),
-                    PQG_BF16 if x.dtype == torch.bfloat16 else PQG_FP16, OUT_DTYPES[out_dtype],
-                    SCALE_FMTS[scale_fmt], LAYOUTS[layout], getattr(stream, "cuda_stream", stream))
-    if st != PQG_OK:
-        raise PqgError(st, "pqg_rmsnorm_quant")
-    return out, scales, x if residual is None else residual_out
+    return _call((_native or native()).rmsnorm_quant, stream, getattr(x, "device", None), x,
+                 weight, residual, out, scales, residual_out, eps, group, OUT_DTYPES[out_dtype],
+                 SCALE_FMTS[scale_fmt], LAYOUTS[layout], global_scale)
 
 
 # ---- paged 4-bit key/value cache --------------------------------------------
@@ -531,7 +498,7 @@ class KVCache:
     """A paged 4-bit cache: its buffers and their geometry (see ``kv_cache``)."""
 
     __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "global_scale", "fmt", "device",
-                 "num_pages", "page_size", "kv_heads", "head_dim", "struct")
+                 "num_pages", "page_size", "kv_heads", "head_dim", "struct", "address", "index")
 
 
 def kv_cache(k_codes, v_codes, k_scales, v_scales, *, fmt: str = "mxfp4",
@@ -574,6 +541,7 @@ def kv_cache(k_codes, v_codes, k_scales, v_scales, *, fmt: str = "mxfp4",
         k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
         None if global_scale is None else global_scale.data_ptr(), pages, size, heads, 2 * half,
         KV_FORMATS[fmt])
+    c.address, c.index = ctypes.addressof(c.struct), dev.index
     return c
 
 
@@ -591,41 +559,6 @@ def kv_allocate(num_pages: int, page_size: int, kv_heads: int, head_dim: int, *,
     return kv_cache(k, v, ks, vs, fmt=fmt, global_scale=global_scale)
 
 
-def _token_stride(t, heads: int, dim: int, name: str, cache) -> int:
-    """Elements between the tokens of [T, heads, dim] with dense heads."""
-    import torch
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [tokens, {heads}, {dim}]")
-    if t.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"unsupported dtype {t.dtype} of {name}")
-    if t.device != cache.device:
-        raise ValueError(f"{name} must be on the cache's device")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
-        raise ValueError(f"the heads of a token of {name} must be dense")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
-
-
-def _index_tensor(t, name: str, cache, numel: int | None = None) -> int:
-    import torch
-    if (t.dtype != torch.int32 or t.device != cache.device or not t.is_contiguous()
-            or (numel is not None and t.numel() != numel)):
-        raise ValueError(f"{name} must be a contiguous int32 tensor"
-                         + ("" if numel is None else f" of {numel} entries")
-                         + " on the cache's device")
-    return t.data_ptr()
-
-
-def _page_table(t, cache):
-    """(address, row stride, columns, rows) of an int32 page table [B, max_pages]."""
-    import torch
-    if (t.dim() != 2 or t.dtype != torch.int32 or t.device != cache.device or t.shape[1] < 1
-            or (t.shape[1] > 1 and t.stride(1) != 1)):
-        raise ValueError("page_table must be an int32 tensor [sequences, pages] on the cache's "
-                         "device with dense rows")
-    rows, width = t.shape
-    return t.data_ptr(), t.stride(0) if rows > 1 else width, width, rows
-
-
 def kv_write(cache: KVCache, k, v, slots, *, stream=None) -> None:
     """Quantize the keys and values of T tokens into their slots of the cache.
 
@@ -635,20 +568,8 @@ def kv_write(cache: KVCache, k, v, slots, *, stream=None) -> None:
     slot outside the cache (-1: padding) is skipped.  Slots of one call must be
     distinct.
     """
-    import torch
-    ks = _token_stride(k, cache.kv_heads, cache.head_dim, "k", cache)
-    vs = _token_stride(v, cache.kv_heads, cache.head_dim, "v", cache)
-    T = k.shape[0]
-    if v.shape[0] != T or v.dtype != k.dtype:
-        raise ValueError("k and v must hold the same tokens in the same dtype")
-    sp = _index_tensor(slots, "slots", cache, T)
-    if stream is None:
-        stream = torch.cuda.current_stream(cache.device)
-    st = _on_device(cache.device, pqg_kv_write, cache.struct, k.data_ptr(), v.data_ptr(), sp, T,
-                    ks, vs, PQG_BF16 if k.dtype == torch.bfloat16 else PQG_FP16,
-                    getattr(stream, "cuda_stream", stream))
-    if st != PQG_OK:
-        raise PqgError(st, "pqg_kv_write")
+    _call((_native or native()).kv_write, stream, cache.device, cache.address, cache.index, k, v,
+          slots)
 
 
 def kv_read(cache: KVCache, page_table, indptr, num_tokens: int, *, dtype=None, k_out=None,
@@ -662,33 +583,13 @@ def kv_read(cache: KVCache, page_table, indptr, num_tokens: int, *, dtype=None, 
     tokens of a page outside the cache read as zeros.  ``dtype`` (bf16 by
     default) is that of the tensors allocated here.
     """
-    import torch
-    tp, stride, width, B = _page_table(page_table, cache)
-    ip = _index_tensor(indptr, "indptr", cache, B + 1)
-    shape = (num_tokens, cache.kv_heads, cache.head_dim)
-    given = k_out if k_out is not None else v_out
-    if given is not None and dtype not in (None, given.dtype):
-        raise ValueError("dtype differs from the given output's")
-    dtype = given.dtype if given is not None else dtype or torch.bfloat16
-    if dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"unsupported dtype {dtype}")
-    with _allocating_on(stream, cache.device):
-        k_out = torch.empty(shape, dtype=dtype, device=cache.device) if k_out is None else k_out
-        v_out = torch.empty(shape, dtype=dtype, device=cache.device) if v_out is None else v_out
-    for name, t in (("k_out", k_out), ("v_out", v_out)):
-        if (tuple(t.shape) != shape or t.dtype != dtype or t.device != cache.device
-                or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on the cache's "
-                             f"device")
-    if stream is None:
-        stream = torch.cuda.current_stream(cache.device)
-    st = _on_device(cache.device, pqg_kv_read, cache.struct, tp, stride, width, ip, B,
-                    k_out.data_ptr(), v_out.data_ptr(), num_tokens,
-                    PQG_BF16 if dtype == torch.bfloat16 else PQG_FP16,
-                    getattr(stream, "cuda_stream", stream))
-    if st != PQG_OK:
-        raise PqgError(st, "pqg_kv_read")
-    return k_out, v_out
+    if dtype is not None:
+        name = str(dtype).removeprefix("torch.")
+        if name not in ("bfloat16", "float16"):
+            raise TypeError(f"unsupported dtype {dtype}")
+        dtype = PQG_BF16 if name == "bfloat16" else PQG_FP16
+    return _call((_native or native()).kv_read, stream, cache.device, cache.address, cache.index,
+                 page_table, indptr, num_tokens, dtype, k_out, v_out)
 
 
 def kv_attention(q, cache: KVCache, page_table, seq_lens, *, sm_scale: float | None = None,
@@ -707,44 +608,8 @@ def kv_attention(q, cache: KVCache, page_table, seq_lens, *, sm_scale: float | N
     gives zeros and -inf.  ``max_len``, the longest sequence's length, is a hint
     for splitting the keys among blocks (0: the page table's capacity).
     """
-    import torch
-    tp, stride, width, B = _page_table(page_table, cache)
-    if q.dim() != 3 or q.shape[1] % cache.kv_heads or q.shape[1] < 1:
-        raise ValueError("q must be [tokens, heads, head_dim] with a multiple of the cache's "
-                         "heads")
-    T, heads, dim = q.shape
-    qs = _token_stride(q, heads, cache.head_dim, "q", cache)
-    sp = _index_tensor(seq_lens, "seq_lens", cache, B)
-    if (T % B if B else T):
-        raise ValueError("q must hold the same number of tokens of each sequence")
-    q_len = T // B if B else 1
-    if q_len < 1:
-        raise ValueError("q must hold at least one token of each sequence")
-    with _allocating_on(stream, cache.device):
-        if out is None:
-            out = torch.empty((T, heads, dim), dtype=q.dtype, device=cache.device)
-        if lse is None and return_lse:
-            lse = torch.empty((T, heads), dtype=torch.float32, device=cache.device)
-        nbytes = pqg_kv_attention_workspace(cache.struct, width, B, q_len, heads, max_len)
-        if nbytes < 0:
-            raise PqgError(nbytes, "pqg_kv_attention_workspace")
-        work = torch.empty(nbytes, dtype=torch.uint8, device=cache.device) if nbytes else None
-    if (tuple(out.shape) != (T, heads, dim) or out.dtype != q.dtype or out.device != cache.device
-            or not out.is_contiguous()):
-        raise ValueError(f"out must be a contiguous {q.dtype} tensor {(T, heads, dim)} on the "
-                         f"cache's device")
-    if lse is not None and (tuple(lse.shape) != (T, heads) or lse.dtype != torch.float32
-                            or lse.device != cache.device or not lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous fp32 tensor {(T, heads)} on the cache's device")
-    if stream is None:
-        stream = torch.cuda.current_stream(cache.device)
-    st = _on_device(cache.device, pqg_kv_attention, cache.struct, q.data_ptr(), qs, tp, stride,
-                    width, sp, B, q_len, heads,
-                    cache.head_dim ** -0.5 if sm_scale is None else float(sm_scale), max_len,
-                    out.data_ptr(), None if lse is None else lse.data_ptr(),
-                    None if work is None else work.data_ptr(), nbytes,
-                    PQG_BF16 if q.dtype == torch.bfloat16 else PQG_FP16,
-                    getattr(stream, "cuda_stream", stream))
-    if st != PQG_OK:
-        raise PqgError(st, "pqg_kv_attention")
-    return out if lse is None else (out, lse)
+    got = _call((_native or native()).kv_attention, stream, cache.device, cache.address,
+                cache.index, q, page_table, seq_lens,
+                cache.head_dim ** -0.5 if sm_scale is None else sm_scale, max_len, out, lse,
+                bool(return_lse))
+    return got if len(got) == 2 else got[0]
