@@ -411,8 +411,8 @@ PQG_API int pqg_kv_attention(const pqg_kv_cache *cache, const void *q, int64_t q
               float sm_scale, int64_t max_len, void *out, float *lse, void *workspace,
               int64_t workspace_bytes, int in_dtype, pqg_stream_t stream);
 
-/* Bytes of scratch pqg_kv_attention needs for these arguments, or a negative
- * pqg_status for arguments it would reject. */
+/* Bytes of scratch pqg_kv_attention needs for these arguments with the same
+ * device current, or a negative pqg_status for arguments it would reject. */
 PQG_API int64_t pqg_kv_attention_workspace(const pqg_kv_cache *cache, int64_t max_pages,
               int64_t B, int64_t q_len, int64_t q_heads, int64_t max_len);
 

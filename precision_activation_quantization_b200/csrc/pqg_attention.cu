@@ -12,20 +12,11 @@ int sm_count(int device);  // cached cudaDevAttrMultiProcessorCount
 
 namespace {
 
-// How a call is cut: row tiles per key/value head, keys per chunk, chunks.
+// How a call is cut: 8-row tiles of a block, units per key/value head, blocks.
 struct Plan {
-    int64_t rows, n_tiles, row_tiles, chunk, chunks, workspace;
+    int64_t rows, n_tiles, row_tiles, units, shares, workspace;
+    bool split;                // whether a unit may be divided among blocks
 };
-
-constexpr int64_t kBlockKeys = 4 * kTileKeys;   // one or two tiles per warp
-#ifndef PQG_ATT_MIN
-#define PQG_ATT_MIN 2
-#endif
-#ifndef PQG_ATT_BLOCKS
-#define PQG_ATT_BLOCKS 16
-#endif
-constexpr int64_t kMinChunk = PQG_ATT_MIN * kBlockKeys;
-constexpr int64_t kTargetBlocks = 148 * PQG_ATT_BLOCKS;
 
 int make_plan(const CacheView &c, int64_t max_pages, int64_t B, int64_t q_len, int64_t q_heads,
               int64_t max_len, Plan *plan) {
@@ -33,43 +24,51 @@ int make_plan(const CacheView &c, int64_t max_pages, int64_t B, int64_t q_len, i
         q_heads % c.heads != 0 || q_heads > kMaxQueryHeads || max_pages < 1 ||
         max_pages >= (int64_t{1} << 31))
         return PQG_ERR_INVALID_ARG;
-    const int64_t cap = std::min<int64_t>(max_pages << c.page_shift, INT32_MAX);
-    const int64_t len = max_len > 0 && max_len < cap ? max_len : cap;
     plan->rows = q_len * (q_heads / c.heads);
     // 16 rows to a block where there are more than 8 (not for a head of 256: registers)
     plan->n_tiles = plan->rows > kTileRows && c.head_dim < 256 ? 2 : 1;
-    plan->row_tiles = (plan->rows + kTileRows * plan->n_tiles - 1) / (kTileRows * plan->n_tiles);
-    const int64_t units = std::max<int64_t>(1, B * c.heads * plan->row_tiles);
-    int64_t chunks = std::max<int64_t>(1, kTargetBlocks / units);
-    chunks = std::min(chunks, (len + kMinChunk - 1) / kMinChunk);
-    plan->chunk = (len + chunks - 1) / chunks;
-    plan->chunk = (plan->chunk + kBlockKeys - 1) / kBlockKeys * kBlockKeys;
-    plan->chunks = (len + plan->chunk - 1) / plan->chunk;
-    if (units * plan->chunks >= (int64_t{1} << 31) ||
-        B * c.heads * plan->rows >= (int64_t{1} << 31))
+    const int64_t rows = kTileRows * plan->n_tiles;
+    plan->row_tiles = (plan->rows + rows - 1) / rows;
+    plan->units = B * c.heads * plan->row_tiles;
+    // one wave of blocks, or fewer where the keys do not give each a piece
+    const int64_t cap = max_pages << c.page_shift;
+    const int64_t len = max_len > 0 && max_len < cap ? max_len : cap;
+    const int64_t pieces = (len + kPieceKeys - 1) / kPieceKeys;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) device = 0;
+    const int64_t wave = static_cast<int64_t>(sm_count(device)) *
+                         (c.head_dim == 64    ? attention_blocks(64, plan->n_tiles)
+                          : c.head_dim == 128 ? attention_blocks(128, plan->n_tiles)
+                                              : attention_blocks(256, plan->n_tiles));
+    plan->shares = plan->units >= wave || pieces >= wave ? wave
+                                                         : std::min(wave, plan->units * pieces);
+    plan->split = cap > kPieceKeys;
+    if (plan->units >= (int64_t{1} << 31) || B * c.heads * plan->rows >= (int64_t{1} << 31))
         return PQG_ERR_INVALID_ARG;
     plan->workspace = 0;
-    if (plan->chunks > 1)
-        plan->workspace = B * c.heads * plan->chunks * plan->rows * (c.head_dim + 2) * 4;
+    if (plan->split && B > 0)
+        plan->workspace = plan->shares * 2 * rows * (c.head_dim + 2) * 4 + plan->units * 8;
     return PQG_OK;
+}
+
+template <typename In, int G, int D, int NT>
+cudaError_t launch_rows(const AttentionParams &p, const Plan &plan, cudaStream_t stream,
+                        int *kernels) {
+    *kernels = 1;
+    const cudaError_t err = launch(attention_kernel<In, G, D, NT>, plan.shares,
+                                   attention_warps(D) * 32, 0, stream, p);
+    if (err != cudaSuccess || !plan.split) return err;
+    *kernels = 2;
+    return launch(attention_join_kernel<In, G, D, NT>,
+                  static_cast<int64_t>(p.B) * p.c.heads * p.rows, kJoinThreads, 0, stream, p);
 }
 
 template <typename In, int G, int D>
 cudaError_t launch_attention(const AttentionParams &p, const Plan &plan, cudaStream_t stream,
                              int *kernels) {
-    const int64_t blocks = static_cast<int64_t>(p.B) * p.c.heads * plan.row_tiles * plan.chunks;
-    cudaError_t err;
     if constexpr (D < 256)
-        err = launch(plan.n_tiles == 2 ? attention_kernel<In, G, D, 2> : attention_kernel<In, G, D, 1>,
-                     blocks, attention_warps(D) * 32, 0, stream, p);
-    else
-        err = launch(attention_kernel<In, G, D, 1>, blocks, attention_warps(D) * 32, 0, stream, p);
-    *kernels = 1;
-    if (err != cudaSuccess || plan.chunks == 1) return err;
-    const int64_t joins = static_cast<int64_t>(p.B) * p.c.heads * p.rows;
-    *kernels = 2;
-    return launch(attention_join_kernel<In, G, D>,
-                  joins, kJoinThreads, 0, stream, p);
+        if (plan.n_tiles == 2) return launch_rows<In, G, D, 2>(p, plan, stream, kernels);
+    return launch_rows<In, G, D, 1>(p, plan, stream, kernels);
 }
 
 template <typename In, int G>
@@ -148,9 +147,13 @@ int pqg_kv_attention(const pqg_kv_cache *cache, const void *q, int64_t q_stride,
     p.out = static_cast<uint8_t *>(out);
     p.lse = lse;
     p.part = static_cast<float *>(workspace);
-    p.stat = plan.workspace == 0
-                 ? nullptr
-                 : reinterpret_cast<float2 *>(p.part + B * p.c.heads * plan.chunks * plan.rows * D);
+    p.stat = nullptr;
+    p.joins = nullptr;
+    if (plan.workspace > 0) {
+        const int64_t places = plan.shares * 2 * kTileRows * plan.n_tiles;
+        p.stat = reinterpret_cast<float2 *>(p.part + places * D);
+        p.joins = reinterpret_cast<uint2 *>(p.stat + places);
+    }
     p.table = page_table;
     p.seq_lens = seq_lens;
     p.q_stride = static_cast<uint64_t>(q_stride);
@@ -162,8 +165,7 @@ int pqg_kv_attention(const pqg_kv_cache *cache, const void *q, int64_t q_stride,
     p.group = static_cast<uint32_t>(q_heads / p.c.heads);
     p.rows = static_cast<uint32_t>(plan.rows);
     p.row_tiles = static_cast<uint32_t>(plan.row_tiles);
-    p.chunk = static_cast<uint32_t>(plan.chunk);
-    p.chunks = static_cast<uint32_t>(plan.chunks);
+    p.shares = static_cast<uint32_t>(plan.shares);
     const bool nv = cache->format == PQG_KV_NVFP4;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int kernels = 0;

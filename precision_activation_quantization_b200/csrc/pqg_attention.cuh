@@ -1,10 +1,13 @@
 // Attention over the paged 4-bit cache, for sm_100a.
 //
-// The keys of a sequence are cut into chunks; a block computes one chunk for the
-// query rows of one key/value head (row r = t * group + h: token t, query head h
-// of the head's group) with a running maximum and sum, and leaves (max, sum,
-// weighted values) in the workspace; a second kernel joins the chunks in their
-// order.  A sequence that fits in one chunk is written out at once.
+// A unit of work is one (sequence, key/value head, tile of 8 or 16 query rows); row
+// r = t * group + h is token t and query head h of the head's group.  Its keys
+// are cut into pieces of 128, and all pieces of all units, in order, are dealt
+// to one wave of blocks in equal shares, so that ragged lengths leave no block
+// behind.  A block computes a unit's pieces in its share with a running maximum
+// and sum; it writes a whole unit's result itself and leaves (maximum, sum,
+// weighted values) of a part of a unit in the workspace, where a second kernel
+// joins the parts in their order.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -20,8 +23,9 @@ struct AttentionParams {
     const uint8_t *q;
     uint8_t *out;
     float *lse;                // or null
-    float *part;               // [B][heads][chunks][rows][D] weighted values, then
-    float2 *stat;              // [B][heads][chunks][rows] (max in log2 units, sum)
+    float *part;               // [2 shares][query rows of a unit][D] weighted values
+    float2 *stat;              // [2 shares][query rows of a unit] (max in log2 units, sum)
+    uint2 *joins;              // [units] (first part's place, parts); 0 parts: written
     const int32_t *table;
     const int32_t *seq_lens;
     uint64_t q_stride;         // elements between tokens
@@ -33,8 +37,7 @@ struct AttentionParams {
     uint32_t group;            // query heads per key/value head
     uint32_t rows;             // q_len * group
     uint32_t row_tiles;
-    uint32_t chunk;            // keys per chunk
-    uint32_t chunks;           // chunks a sequence is dealt to (it may have more keys: they wrap)
+    uint32_t shares;           // blocks
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
@@ -46,9 +49,77 @@ __device__ __forceinline__ uint32_t sequence_length(const AttentionParams &p, ui
     const int n = max(__ldg(p.seq_lens + b), 0);
     return static_cast<uint64_t>(n) < cap ? static_cast<uint32_t>(n) : static_cast<uint32_t>(cap);
 }
-// Chunks that hold keys (0 or 1: the block writes the result itself).
-__device__ __forceinline__ uint32_t used_chunks(const AttentionParams &p, uint32_t n) {
-    return min((n + p.chunk - 1u) / p.chunk, p.chunks);
+// Pieces of a unit of n keys; one without keys is a piece too, which writes zeros.
+constexpr uint32_t kPieceKeys = 128;
+__device__ __forceinline__ uint32_t pieces_of(uint32_t n) {
+    return max((n + kPieceKeys - 1u) / kPieceKeys, 1u);
+}
+
+// A block's share [at, end) of the pieces, and the sequence that holds piece
+// `at`, whose own pieces begin at `first`.  With P pieces in all, s = min(blocks,
+// P) shares have at least one each, and share i begins at floor(i P / s).
+struct Share {
+    uint64_t at, end, total, first;
+    uint32_t b, shares;
+    __device__ __forceinline__ void deal(uint64_t pieces, uint32_t blocks) {
+        total = pieces;
+        shares = static_cast<uint32_t>(min(static_cast<uint64_t>(blocks), pieces));
+        const uint64_t i = min(blockIdx.x, shares);
+        at = i * pieces / shares;
+        end = min(i + 1u, static_cast<uint64_t>(shares)) * pieces / shares;
+    }
+};
+// Every thread of the block calls it.  Each sums the pieces of neighbouring
+// sequences, a prefix sum over the block finds the thread that holds `at`, and
+// that one walks to the sequence.
+template <int THREADS>
+__device__ __forceinline__ Share find_share(const AttentionParams &p, uint32_t units_per_sequence) {
+    Share s;
+    s.b = 0;
+    s.first = 0;
+    if (p.B == 1u) {
+        s.deal(static_cast<uint64_t>(pieces_of(sequence_length(p, 0))) * units_per_sequence,
+               p.shares);
+        return s;
+    }
+    __shared__ uint64_t sums[THREADS / 32], found_first;
+    __shared__ uint32_t found_b;
+    const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+    const uint32_t per = (p.B + THREADS - 1u) / THREADS;
+    const uint32_t lo = min(threadIdx.x * per, p.B), hi = min(lo + per, p.B);
+    uint64_t own = 0;
+    for (uint32_t b = lo; b < hi; ++b) own += pieces_of(sequence_length(p, b));
+    uint64_t incl = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= static_cast<uint32_t>(o)) incl += v;
+    }
+    if (lane == 31u) sums[warp] = incl;
+    __syncthreads();
+    uint64_t before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < static_cast<int>(warp)) before += sums[w];
+        all += sums[w];
+    }
+    s.deal(all * units_per_sequence, p.shares);
+    uint64_t first = (before + incl - own) * units_per_sequence;
+    if (own > 0 && first <= s.at && s.at < first + own * units_per_sequence) {
+        uint32_t b = lo;
+        for (;; ++b) {                         // ends: `at` lies before the pieces' end
+            const uint64_t next =
+                first + static_cast<uint64_t>(pieces_of(sequence_length(p, b))) * units_per_sequence;
+            if (s.at < next || b + 1u >= hi) break;
+            first = next;
+        }
+        found_b = b;
+        found_first = first;
+    }
+    __syncthreads();
+    s.b = found_b;
+    s.first = found_first;
+    return s;
 }
 
 // Warps of a block (a head of 256 takes more shared memory per warp).
@@ -170,7 +241,7 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 }
 
 // ---------------------------------------------------------------------------
-// One chunk
+// A block's share
 // ---------------------------------------------------------------------------
 //
 // Mathematics.  With c_jd the 4-bit code of key j, s_jg its scale and q the
@@ -231,23 +302,32 @@ struct AttentionShape {
     static constexpr int kPad = D + 4;                      // floats of a row in the join
     static constexpr int kJoin = kRows * kPad * 4;
     static constexpr int kWarpBytes = 2 * kTile > kJoin ? 2 * kTile : kJoin;
+    struct Shared {
+        alignas(128) uint8_t ring[kWarps][kWarpBytes];
+        uint2 queries[NT][D / 16][32];                      // the first product's B, per lane
+        float stats[kWarps][kRows][2];
+        float shrinks[kRows];
+    };
 };
 
-// Blocks per SM the registers have to allow.
+// Resident blocks per SM, which the registers are held to and a wave counts on.
 #ifndef PQG_ATT_OCC
 #define PQG_ATT_OCC 4
 #endif
 #ifndef PQG_ATT_OCC2
 #define PQG_ATT_OCC2 3
 #endif
-template <int D, int NT>
-constexpr int attention_blocks() {
-    return D == 64 ? (NT == 1 ? 5 : 4) : D == 128 ? (NT == 1 ? PQG_ATT_OCC : PQG_ATT_OCC2) : 4;
+__host__ __device__ constexpr int attention_blocks(int D, int NT) {
+    return D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? PQG_ATT_OCC : PQG_ATT_OCC2) : 4;
 }
 
+// Query rows [tile * R, + R) of (sequence b, key/value head) over keys [k_begin, k_end)
+// of its n: written out when `whole`, else left at `place` of the workspace.
 template <typename In, int G, int D, int NT>
-__global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, NT>())
-    attention_kernel(const __grid_constant__ AttentionParams p) {
+__device__ __forceinline__ void attend(const AttentionParams &p,
+                                       typename AttentionShape<G, D, NT>::Shared &smem, uint32_t b,
+                                       uint32_t head, uint32_t tile, uint32_t n, uint32_t k_begin,
+                                       uint32_t k_end, bool whole, uint32_t place) {
     using Shape = AttentionShape<G, D, NT>;
     constexpr int W = Shape::kWarps;
     constexpr int KW = D / 32;                 // words of a lane's part of a key
@@ -256,27 +336,9 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
     constexpr int VG = D / 8 > G ? D / 8 / G : 1;
     constexpr int MT = D / 16;                 // m-tiles of the second product
     constexpr int R = Shape::kRows;
-    __shared__ __align__(128) uint8_t ring[W][Shape::kWarpBytes];
-    __shared__ float stats[W][R][2];
-    __shared__ uint2 queries[NT][MT][32];      // the first product's B operand, per lane
-    __shared__ float shrinks[R];
     static_assert(NT <= W, "a warp prepares 8 query rows");
-
-    wait_for_producer();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t gid = lane >> 2, tig = lane & 3u;
-    uint32_t at = blockIdx.x;
-    const uint32_t tile = at % p.row_tiles;
-    at /= p.row_tiles;
-    const uint32_t chunk = at % p.chunks;
-    at /= p.chunks;
-    const uint32_t head = at % p.c.heads, b = at / p.c.heads;
-    const uint32_t n = sequence_length(p, b);
-    const uint32_t used = used_chunks(p, n);
-    if (chunk >= max(used, 1u)) {
-        release_dependents();
-        return;
-    }
 
     float acc[MT][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -298,7 +360,7 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
     const uint32_t code_page = (p.c.heads << p.c.page_shift) * (D / 2);
     const uint32_t scale_page = (p.c.heads << p.c.page_shift) * (D / G);
     const int32_t *table = p.table + static_cast<uint64_t>(b) * p.table_stride;
-    uint8_t *const mine = ring[warp];
+    uint8_t *const mine = smem.ring[warp];
     const uint32_t mine_at = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
     // this lane's 16-byte part of the first rows, in the cache and in the tile; a
     // copy takes kRowsPerCopy rows, and row_at's choice of place for later rows is
@@ -359,27 +421,14 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
                 copy16(to + 2 * Shape::kCodes + (i + lane) * 16u, scale_src[i / 32u] + at);
     };
 
-    // -- the warp's tiles: every W-th of the chunk, and of the chunks that wrap ---
-    const uint64_t lap = static_cast<uint64_t>(p.chunk) * p.chunks;
-    uint64_t first = static_cast<uint64_t>(chunk) * p.chunk;
-    uint32_t in_chunk = warp * kTileKeys;
-    auto next_tile = [&]() {                   // the tile after this one
-        in_chunk += W * kTileKeys;
-        if (in_chunk >= p.chunk) {
-            in_chunk = warp * kTileKeys;
-            first += lap;
-        }
-        return first + in_chunk;
-    };
+    // -- the warp's tiles: every W-th ----------------------------------------------
     // pages are read a tile before the copies that need them
-    uint64_t j64 = first + in_chunk, next64 = 0;
+    uint32_t j = k_begin + warp * kTileKeys;
     int pg[2] = {-1, -1}, pg_next[2] = {-1, -1};
-    bool more = j64 < n;
-    if (more) {
-        pages(static_cast<uint32_t>(j64), pg);
-        next64 = next_tile();
-        if (next64 < n) pages(static_cast<uint32_t>(next64), pg_next);
-        copy_tile(static_cast<uint32_t>(j64), pg, 0u);   // (a page outside the cache becomes -1)
+    if (j < k_end) {
+        pages(j, pg);
+        if (j + W * kTileKeys < k_end) pages(j + W * kTileKeys, pg_next);
+        copy_tile(j, pg, 0u);                  // (a page outside the cache becomes -1)
     }
     commit_copies();
     // -- the query rows, normalised: a warp each for 8 of them, while tiles come ---
@@ -408,14 +457,14 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
         const int up = min(max(268 - e, 14), 253);
         const float grow = __uint_as_float(static_cast<uint32_t>(up) << 23);
         if (tig == 0u)
-            shrinks[warp * kTileRows + gid] =
+            smem.shrinks[warp * kTileRows + gid] =
                 __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             float x0, x1, x2, x3;
             widen2<In>(raw[2 * i], x0, x1);
             widen2<In>(raw[2 * i + 1], x2, x3);
-            queries[warp][i][lane] = make_uint2(narrow2<__half>(x0 * grow, x1 * grow),
+            smem.queries[warp][i][lane] = make_uint2(narrow2<__half>(x0 * grow, x1 * grow),
                                                 narrow2<__half>(x2 * grow, x3 * grow));
         }
     }
@@ -428,7 +477,7 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const uint32_t col = nt * kTileRows + 2u * tig + k;
-            head_scale[nt][k] = shrinks[col] * (p.scale_log2 * inv_k);
+            head_scale[nt][k] = smem.shrinks[col] * (p.scale_log2 * inv_k);
             limit[nt][k] = static_cast<int>(n) - static_cast<int>(p.q_len - 1u) +
                            static_cast<int>(min((tile * R + col) / p.group, p.q_len - 1u));
         }
@@ -449,18 +498,15 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
                   (gid * (D / 16)) % 16u;
     }
     uint32_t buffer = 0;
-    while (more) {
-        const uint32_t j = static_cast<uint32_t>(j64);
+    for (; j < k_end; j += W * kTileKeys) {
         const int now[2] = {pg[0], pg[1]};
         // the other buffer's tile is done with (the loop ends in __syncwarp)
-        j64 = next64;
-        more = j64 < n;
+        const uint32_t next = j + W * kTileKeys;
         pg[0] = pg_next[0];
         pg[1] = pg_next[1];
-        if (more) {
-            copy_tile(static_cast<uint32_t>(j64), pg, buffer ^ 1u);
-            next64 = next_tile();
-            if (next64 < n) pages(static_cast<uint32_t>(next64), pg_next);
+        if (next < k_end) {
+            copy_tile(next, pg, buffer ^ 1u);
+            if (next + W * kTileKeys < k_end) pages(next + W * kTileKeys, pg_next);
         }
         commit_copies();
         wait_copies<1>();
@@ -476,18 +522,17 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
             load_shared(scales_at + tile_at + v_scale_at + g * kTileKeys, vsc[g]);
 
         // a tile some of whose keys some row does not see (warp-uniform)
-        const bool edge =
-            static_cast<int>(j + kTileKeys) > static_cast<int>(n - (p.q_len - 1u)) ||
-            now[0] < 0 || now[1] < 0;
         const int live = static_cast<int>(n - j);          // tokens of the tile in the sequence
+        const bool edge = live < kTileKeys + static_cast<int>(p.q_len - 1u) || now[0] < 0 ||
+                          now[1] < 0;
         if (edge) {                            // scales of keys that are not there may be anything
-            const int k_end = (gid < 4u ? now[0] : now[1]) < 0 ? 0 : live, v_end = (tig < 2u ? now[0] : now[1]) < 0 ? 0 : live;
+            const int k_live = (gid < 4u ? now[0] : now[1]) < 0 ? 0 : live, v_live = (tig < 2u ? now[0] : now[1]) < 0 ? 0 : live;
 #pragma unroll
-            for (int g = 0; g < KG; ++g) ksc[g] = keep_bytes(ksc[g], k_first, k_end);
+            for (int g = 0; g < KG; ++g) ksc[g] = keep_bytes(ksc[g], k_first, k_live);
 #pragma unroll
             for (int g = 0; g < VG; ++g) {
-                vsc[g][0] = keep_bytes(vsc[g][0], v_first, v_end);
-                vsc[g][1] = keep_bytes(vsc[g][1], v_first + 4, v_end);
+                vsc[g][0] = keep_bytes(vsc[g][0], v_first, v_live);
+                vsc[g][1] = keep_bytes(vsc[g][1], v_first + 4, v_live);
             }
         }
 
@@ -541,8 +586,8 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
             uint2 q[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                q[nt][0] = queries[nt][2 * w][lane];
-                q[nt][1] = queries[nt][2 * w + 1][lane];
+                q[nt][0] = smem.queries[nt][2 * w][lane];
+                q[nt][1] = smem.queries[nt][2 * w + 1][lane];
             }
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
@@ -578,7 +623,7 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
                         if ((gid < 4u ? now[0] : now[1]) < 0 ||
-                            static_cast<int>(j + k_first + x) >= limit[nt][k])
+                            static_cast<int>(k_first + x) >= limit[nt][k] - static_cast<int>(j))
                             s[x][k] = -INFINITY;
             }
             float top[2];
@@ -682,7 +727,7 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
     __syncwarp();                              // the buffers are free for the join
 
     // -- join the block's warps ----------------------------------------------------------
-    const float unit = G == 16 ? 1.0f : exp2f(static_cast<float>(vref) - 139.0f);
+    const float grain = G == 16 ? 1.0f : exp2f(static_cast<float>(vref) - 139.0f);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -691,13 +736,13 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
             for (int o = 4; o < 32; o <<= 1) l[nt][k] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][k], o);
             const uint32_t r = nt * kTileRows + 2u * tig + k;
             if (gid == 0) {
-                stats[warp][r][0] = m[nt][k];
-                stats[warp][r][1] = l[nt][k];
+                smem.stats[warp][r][0] = m[nt][k];
+                smem.stats[warp][r][1] = l[nt][k];
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i)
                 *reinterpret_cast<float2 *>(mine + (r * Shape::kPad + gid * (D / 8) + 2 * i) * 4) =
-                    make_float2(acc[i][nt][k] * unit, acc[i][nt][k + 2] * unit);
+                    make_float2(acc[i][nt][k] * grain, acc[i][nt][k + 2] * grain);
         }
     }
     __syncthreads();
@@ -707,17 +752,17 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
         if (row >= p.rows) break;
         float top = kNoMax, sum = 0.0f, x = 0.0f, y = 0.0f;
 #pragma unroll
-        for (int w = 0; w < W; ++w) top = fmaxf(top, stats[w][r][0]);
+        for (int w = 0; w < W; ++w) top = fmaxf(top, smem.stats[w][r][0]);
 #pragma unroll
         for (int w = 0; w < W; ++w) {
-            const float f = ex2_approx(stats[w][r][0] - top);
+            const float f = ex2_approx(smem.stats[w][r][0] - top);
             const float2 o =
-                *reinterpret_cast<const float2 *>(ring[w] + (r * Shape::kPad + d) * 4);
-            sum = fmaf(stats[w][r][1], f, sum);
+                *reinterpret_cast<const float2 *>(smem.ring[w] + (r * Shape::kPad + d) * 4);
+            sum = fmaf(smem.stats[w][r][1], f, sum);
             x = fmaf(o.x, f, x);
             y = fmaf(o.y, f, y);
         }
-        if (used <= 1u) {
+        if (whole) {
             const uint32_t t = row / p.group, qh = head * p.group + (row - t * p.group);
             const uint64_t slot =
                 (static_cast<uint64_t>(b) * p.q_len + t) * p.c.heads * p.group + qh;
@@ -727,11 +772,50 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
             if (d == 0u && p.lse != nullptr)
                 p.lse[slot] = sum > 0.0f ? (top - 7.0f + log2f(sum)) * kLn2 : -INFINITY;
         } else {
-            const uint64_t slot =
-                ((static_cast<uint64_t>(b) * p.c.heads + head) * p.chunks + chunk) * p.rows + row;
-            *reinterpret_cast<float2 *>(p.part + slot * D + d) = make_float2(x, y);
-            if (d == 0u) p.stat[slot] = make_float2(top, sum);
+            const uint64_t at = static_cast<uint64_t>(place) * R + r;
+            *reinterpret_cast<float2 *>(p.part + at * D + d) = make_float2(x, y);
+            if (d == 0u) p.stat[at] = make_float2(top, sum);
         }
+    }
+}
+
+template <typename In, int G, int D, int NT>
+__global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks(D, NT))
+    attention_kernel(const __grid_constant__ AttentionParams p) {
+    using Shape = AttentionShape<G, D, NT>;
+    __shared__ typename Shape::Shared smem;
+    wait_for_producer();
+    const uint32_t units = p.c.heads * p.row_tiles;          // of a sequence
+    Share share = find_share<Shape::kThreads>(p, units);
+    for (const uint64_t first = share.at; share.at < share.end;) {
+        // the unit that holds piece `at`, and its pieces in the share
+        const uint32_t n = sequence_length(p, share.b), pieces = pieces_of(n);
+        const uint64_t within = share.at - share.first;
+        const uint32_t unit = static_cast<uint32_t>(within / pieces);
+        const uint32_t piece = static_cast<uint32_t>(within - static_cast<uint64_t>(unit) * pieces);
+        const uint32_t taken =
+            static_cast<uint32_t>(min(static_cast<uint64_t>(pieces - piece), share.end - share.at));
+        // a share's first unit may have begun in another share, its last may end in one
+        const uint32_t place = 2u * blockIdx.x + (share.at == first ? 0u : 1u);
+        const uint32_t head = unit / p.row_tiles;
+        attend<In, G, D, NT>(p, smem, share.b, head, unit - head * p.row_tiles, n,
+                             piece * kPieceKeys, min(n, (piece + taken) * kPieceKeys),
+                             taken == pieces, place);
+        // the block that holds a unit's first piece says where its parts are: its own
+        // place, then one in every share up to the last that begins before the unit's end
+        if (piece == 0u && threadIdx.x == 0u && p.joins != nullptr) {
+            const uint64_t end = share.at + pieces;
+            const uint32_t last =
+                static_cast<uint32_t>((end * share.shares - 1u) / share.total);
+            p.joins[static_cast<uint64_t>(share.b) * units + unit] =
+                make_uint2(place, taken == pieces ? 0u : last - blockIdx.x + 1u);
+        }
+        share.at += taken;
+        if (piece + taken == pieces && unit + 1u == units) {
+            ++share.b;
+            share.first = share.at;
+        }
+        __syncthreads();                       // the next unit reuses the buffers
     }
     release_dependents();
 }
@@ -739,33 +823,38 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks<D, N
 constexpr int kJoinWarps = 4;
 constexpr int kJoinThreads = kJoinWarps * 32;
 
-// Joins the chunks of one (sequence, query row): a block per row, whose warps
-// take every fourth chunk each.  The order of the sums is fixed.
-template <typename In, int G, int D>
+// Joins the parts of one query row's unit: a block per row, whose warps take every
+// fourth part each.  The order of the sums is fixed.
+template <typename In, int G, int D, int NT>
 __global__ void __launch_bounds__(kJoinThreads)
     attention_join_kernel(const __grid_constant__ AttentionParams p) {
     constexpr int E = D / 32;                  // elements a lane sums
+    constexpr uint32_t R = NT * kTileRows;
     __shared__ float sums[kJoinWarps][D];
     wait_for_producer();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t r = blockIdx.x % p.rows, bh = blockIdx.x / p.rows;
     const uint32_t head = bh % p.c.heads, b = bh / p.c.heads;
-    const uint32_t used = used_chunks(p, sequence_length(p, b));
+    const uint2 join = p.joins[static_cast<uint64_t>(bh) * p.row_tiles + r / R];
+    const uint32_t used = join.y;
     if (used > 1u) {
-        const uint64_t slot = static_cast<uint64_t>(bh) * p.chunks * p.rows + r;
+        // part 0, then the first place of each later share
+        auto part_at = [&](uint32_t c) {
+            return static_cast<uint64_t>(c == 0u ? join.x : (join.x / 2u + c) * 2u) * R + r % R;
+        };
         float m = kNoMax, l = 0.0f, acc[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = 0.0f;
         for (uint32_t c = lane; c < used; c += 32u)
-            m = fmaxf(m, p.stat[slot + static_cast<uint64_t>(c) * p.rows].x);
+            m = fmaxf(m, p.stat[part_at(c)].x);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        // 32 chunks at a time: a lane holds one chunk's factor, and every warp
+        // 32 parts at a time: a lane holds one part's factor, and every warp
         // adds the values of 8 of them
         for (uint32_t c0 = 0; c0 < used; c0 += 32u) {
             float f = 0.0f;
             if (c0 + lane < used) {
-                const float2 st = p.stat[slot + static_cast<uint64_t>(c0 + lane) * p.rows];
+                const float2 st = p.stat[part_at(c0 + lane)];
                 f = ex2_approx(st.x - m);
                 l = fmaf(st.y, f, l);
             }
@@ -776,7 +865,7 @@ __global__ void __launch_bounds__(kJoinThreads)
                 if (c < used) {                // warp-uniform
                     uint32_t v[E];
                     load_words(reinterpret_cast<const uint8_t *>(
-                                   p.part + (slot + static_cast<uint64_t>(c) * p.rows) * D + lane * E),
+                                   p.part + part_at(c) * D + lane * E),
                                v);
 #pragma unroll
                     for (int k = 0; k < E; ++k) acc[k] = fmaf(__uint_as_float(v[k]), fc, acc[k]);

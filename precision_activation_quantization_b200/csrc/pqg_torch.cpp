@@ -310,6 +310,7 @@ PyObject *py_kv_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
     const int64_t q_len = B > 0 ? T / B : 1;
     const double sm_scale = number(a[5], "sm_scale");
     const int64_t max_len = integer(a[6], "max_len");
+    const c10::cuda::CUDAGuard guard(cache.device);   // the scratch goes by the current device
     const int64_t bytes =
         lib.kv_attention_workspace(cache.c, table.width, B, q_len, heads, max_len);
     if (bytes < 0) return result(bytes, "pqg_kv_attention_workspace", {});
@@ -327,7 +328,6 @@ PyObject *py_kv_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
         lse = empty({T, heads}, at::kFloat, cache.device);
     }
     if (bytes > 0) work = empty({bytes}, at::kByte, cache.device);
-    const c10::cuda::CUDAGuard guard(cache.device);
     const int status = lib.kv_attention(
         cache.c, q.data_ptr(), stride, table.p, table.stride, table.width, lens, B, q_len, heads,
         static_cast<float>(sm_scale), max_len, out.data_ptr(),

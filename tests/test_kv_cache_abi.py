@@ -116,7 +116,7 @@ def test_struct_and_formats_match_the_header():
 
 
 def attend(c=None, **kw):
-    a = dict(q_ptr=at(4), q_stride=1024, page_table_ptr=at(5), table_stride=3, max_pages=3,
+    a = dict(q_ptr=at(4), q_stride=1024, page_table_ptr=at(5), table_stride=2, max_pages=2,
              seq_lens_ptr=at(6), B=2, q_len=1, q_heads=8, sm_scale=0.1, max_len=0, out_ptr=at(7),
              lse_ptr=at(8), workspace_ptr=None, workspace_bytes=0, in_dtype=pqg.PQG_BF16,
              stream=None)
@@ -138,7 +138,7 @@ LONG = dict(max_pages=4096, table_stride=4096)      # 262144 keys: split, needs 
 @pytest.mark.parametrize("kw,status", [
     (dict(in_dtype=2), INV), (dict(B=-1), INV), (dict(B=1 << 21), INV), (dict(q_len=0), INV),
     (dict(q_len=1025), INV), (dict(q_heads=7), INV), (dict(q_heads=0), INV),
-    (dict(q_heads=16386), INV), (dict(max_pages=0), INV), (dict(table_stride=2), INV),
+    (dict(q_heads=16386), INV), (dict(max_pages=0), INV), (dict(table_stride=1), INV),
     (dict(sm_scale=float("nan")), INV), (dict(sm_scale=float("inf")), INV),
     (dict(q_stride=1016), INV), (dict(q_stride=1 << 33), INV), (dict(q_stride=1028), ALN),
     (dict(q_ptr=0), INV), (dict(page_table_ptr=0), INV), (dict(seq_lens_ptr=0), INV),
@@ -164,8 +164,8 @@ def test_attention_nothing_to_do_and_scratch():
     assert attend(B=0, q_ptr=0, out_ptr=0, page_table_ptr=0, seq_lens_ptr=0) == pqg.PQG_OK
     assert pqg.pqg_launch_count() == before
     work = pqg.pqg_kv_attention_workspace
-    assert work(cache(), 3, 2, 1, 8, 0) == 0                        # short: written at once
-    assert work(cache(), 4096, 2, 1, 8, 0) > 0
-    assert work(cache(), 4096, 2, 1, 8, 100) == 0                   # by the hint
+    assert work(cache(), 2, 2, 1, 8, 0) == 0                        # 128 keys: never divided
+    assert work(cache(), 3, 2, 1, 8, 0) > 0
+    assert work(cache(), 4096, 2, 1, 8, 100) > 0                    # the hint is no promise
     assert work(cache(), 4096, 0, 1, 8, 0) == 0
     assert work(cache(), 4096, 2, 1, 7, 0) == INV
