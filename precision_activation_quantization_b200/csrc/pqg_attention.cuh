@@ -217,21 +217,17 @@ __device__ __forceinline__ void wait_copies() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The largest of the four bytes of each word.
-template <int N>
-__device__ __forceinline__ uint32_t max_byte(const uint32_t (&w)[N]) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        m = __vimax3_u16x2(m, w[i] & 0x00FF00FFu, (w[i] >> 8) & 0x00FF00FFu);
-    return max(m & 0xFFFFu, m >> 16);
-}
+// The larger half of a pair of 16-bit numbers.
+__device__ __forceinline__ uint32_t larger_half(uint32_t v) { return max(v & 0xFFFFu, v >> 16); }
 
 // 2^(e - ref + 12) in binary16 for two UE8M0 bytes (in bits 0-7 and 16-23) that
-// are at most ref; 0 where the power is below 2^-14.
-__device__ __forceinline__ uint32_t relative_power2(uint32_t e2, uint32_t ref) {
-    const uint32_t shift = (27u - ref) & 0xFFFFu;
-    return __viaddmax_s16x2(e2, shift | (shift << 16), 0u) << 10;
+// are at most ref, which comes as reference2(ref); 0 where the power is below 2^-14.
+__device__ __forceinline__ uint32_t relative_power2(uint32_t e2, uint32_t ref2) {
+    return __viaddmax_s16x2(e2, ref2, 0u) << 10;
+}
+// The second argument for a reference exponent.
+__device__ __forceinline__ uint32_t reference2(uint32_t ref) {
+    return ((27u - ref) & 0xFFFFu) * 0x00010001u;
 }
 
 // A word's bytes [from, from + 4) of a tile, those at or past `end` zeroed.
@@ -353,7 +349,8 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
 #pragma unroll
             for (int k = 0; k < 4; ++k) acc[i][nt][k] = 0.0f;
     }
-    uint32_t vref = 0u;                        // MXFP4: the values' reference exponent
+    // MXFP4: the reference exponents of the keys and of this lane's values so far
+    uint32_t kref = 0u, vref = 0u;
 
     // -- copying a tile -----------------------------------------------------------
     const uint32_t page_mask = (1u << p.c.page_shift) - 1u;
@@ -469,7 +466,9 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
         }
     }
     __syncthreads();
-    float head_scale[NT][2];                   // of this lane's columns 2 tig, 2 tig + 1
+    // factors of a score, of this lane's columns 2 tig and 2 tig + 1: of the query and,
+    // MXFP4, of the query and the keys' reference
+    float head_scale[NT][2], scale[NT][2];
     int limit[NT][2];                          // keys they see
     const float inv_k = G == 16 ? __frcp_rn(__ldg(p.c.gscale)) : 1.0f;
 #pragma unroll
@@ -478,6 +477,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
         for (int k = 0; k < 2; ++k) {
             const uint32_t col = nt * kTileRows + 2u * tig + k;
             head_scale[nt][k] = smem.shrinks[col] * (p.scale_log2 * inv_k);
+            scale[nt][k] = head_scale[nt][k];
             limit[nt][k] = static_cast<int>(n) - static_cast<int>(p.q_len - 1u) +
                            static_cast<int>(min((tile * R + col) / p.group, p.q_len - 1u));
         }
@@ -512,6 +512,13 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
         wait_copies<1>();
         __syncwarp();
         const uint32_t tile_at = buffer * Shape::kTile;
+        // a tile some of whose keys some row does not see (warp-uniform; two copies of
+        // the body, so that the others carry no test of it)
+        const int live = static_cast<int>(n - j);          // tokens of the tile in the sequence
+        const bool edge = live < kTileKeys + static_cast<int>(p.q_len - 1u) || now[0] < 0 ||
+                          now[1] < 0;
+        auto body = [&](auto edge_tag) {
+        constexpr bool EDGE = decltype(edge_tag)::value;
         uint32_t ksc[KG], vsc[VG][2];
 #pragma unroll
         for (int g = 0; g < KG; ++g)
@@ -520,13 +527,9 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
 #pragma unroll
         for (int g = 0; g < VG; ++g)
             load_shared(scales_at + tile_at + v_scale_at + g * kTileKeys, vsc[g]);
-
-        // a tile some of whose keys some row does not see (warp-uniform)
-        const int live = static_cast<int>(n - j);          // tokens of the tile in the sequence
-        const bool edge = live < kTileKeys + static_cast<int>(p.q_len - 1u) || now[0] < 0 ||
-                          now[1] < 0;
-        if (edge) {                            // scales of keys that are not there may be anything
-            const int k_live = (gid < 4u ? now[0] : now[1]) < 0 ? 0 : live, v_live = (tig < 2u ? now[0] : now[1]) < 0 ? 0 : live;
+        if constexpr (EDGE) {                  // scales of keys that are not there may be anything
+            const int k_live = (gid < 4u ? now[0] : now[1]) < 0 ? 0 : live;
+            const int v_live = (tig < 2u ? now[0] : now[1]) < 0 ? 0 : live;
 #pragma unroll
             for (int g = 0; g < KG; ++g) ksc[g] = keep_bytes(ksc[g], k_first, k_live);
 #pragma unroll
@@ -537,7 +540,6 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
         }
 
         // -- scores: 32 tokens x rows ----------------------------------------------
-        float tile_scale = 1.0f;
         uint32_t ks[KG][4];                    // a token's scale, twice
         if constexpr (G == 16) {
 #pragma unroll
@@ -545,20 +547,32 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                 uint32_t h[2];
                 decode_e4m3x4(ksc[g], h);
 #pragma unroll
-                for (int x = 0; x < 4; ++x) ks[g][x] = __byte_perm(h[x >> 1], 0, x & 1 ? 0x3232 : 0x1010);
+                for (int x = 0; x < 4; ++x)
+                    ks[g][x] = __byte_perm(h[x >> 1], 0, x & 1 ? 0x3232 : 0x1010);
             }
         } else {
-            const uint32_t kref = __reduce_max_sync(0xFFFFFFFFu, max_byte(ksc));
+            uint32_t top = kref * 0x00010001u;
+#pragma unroll
+            for (int g = 0; g < KG; ++g)
+                top = __vimax3_u16x2(top, ksc[g] & 0x00FF00FFu, (ksc[g] >> 8) & 0x00FF00FFu);
+            if (__any_sync(0xFFFFFFFFu, top != kref * 0x00010001u)) {
+                kref = __reduce_max_sync(0xFFFFFFFFu, larger_half(top));
+                // 2^(kref - 127 - 12); below 2^-126 the scores are nothing
+                const float unit = kref > 12u ? __uint_as_float((kref - 12u) << 23) : 0.0f;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) scale[nt][k] = head_scale[nt][k] * unit;
+            }
+            const uint32_t ref2 = reference2(kref);
 #pragma unroll
             for (int g = 0; g < KG; ++g) {
-                const uint32_t even = relative_power2(ksc[g] & 0x00FF00FFu, kref);
-                const uint32_t odd = relative_power2((ksc[g] >> 8) & 0x00FF00FFu, kref);
+                const uint32_t even = relative_power2(ksc[g] & 0x00FF00FFu, ref2);
+                const uint32_t odd = relative_power2((ksc[g] >> 8) & 0x00FF00FFu, ref2);
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     ks[g][x] = __byte_perm(x & 1 ? odd : even, 0, x & 2 ? 0x3232 : 0x1010);
             }
-            // 2^(kref - 127 - 12); below 2^-126 the scores are nothing
-            tile_scale = kref > 12u ? __uint_as_float((kref - 12u) << 23) : 0.0f;
         }
         uint32_t kraw[4][KW];
 #pragma unroll
@@ -611,13 +625,12 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
         uint32_t weights[NT][4];               // B operand: [2 * k-step + half]
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float f[2] = {head_scale[nt][0] * tile_scale, head_scale[nt][1] * tile_scale};
             float s[4][2];                     // [token][column]
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) s[x][k] = c[x >> 1][nt][2 * (x & 1) + k] * f[k];
-            if (edge) {
+                for (int k = 0; k < 2; ++k) s[x][k] = c[x >> 1][nt][2 * (x & 1) + k] * scale[nt][k];
+            if constexpr (EDGE) {
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
@@ -672,11 +685,17 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
             }
         } else {
             static_assert(G == 16 || VG == 1, "one reference exponent per lane");
-            uint32_t top = max_byte(vsc[0]);
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            if (__any_sync(0xFFFFFFFFu, top > vref)) {
-                const uint32_t next = max(vref, top);
+            // scales of tokens x and x + 4, 16 bits each
+            const uint32_t first = __byte_perm(vsc[0][0], vsc[0][1], 0x5410);
+            const uint32_t last = __byte_perm(vsc[0][0], vsc[0][1], 0x7632);
+            uint32_t e[4] = {first & 0x00FF00FFu, (first >> 8) & 0x00FF00FFu, last & 0x00FF00FFu,
+                             (last >> 8) & 0x00FF00FFu};
+            uint32_t top = __vimax3_u16x2(e[0], e[1], vref * 0x00010001u);
+            top = __vimax3_u16x2(e[2], e[3], top);
+            if (__any_sync(0xFFFFFFFFu, top != vref * 0x00010001u)) {
+                uint32_t next = larger_half(top);
+                next = max(next, __shfl_xor_sync(0xFFFFFFFFu, next, 1));
+                next = max(next, __shfl_xor_sync(0xFFFFFFFFu, next, 2));
                 const float fade = ex2_approx(-static_cast<float>(next - vref));
                 vref = next;
 #pragma unroll
@@ -687,9 +706,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                         for (int k = 0; k < 4; ++k) acc[i][nt][k] *= fade;
             }
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                vs[0][x] = relative_power2(
-                    __byte_perm(vsc[0][0], vsc[0][1], (x + 4) << 8 | x) & 0x00FF00FFu, vref);
+            for (int x = 0; x < 4; ++x) vs[0][x] = relative_power2(e[x], reference2(vref));
         }
         uint32_t vraw[8][VW];
 #pragma unroll
@@ -720,6 +737,9 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                                  weights[nt][2 * ks2], weights[nt][2 * ks2 + 1]);
             }
         }
+        };
+        if (edge) body(std::true_type{});
+        else body(std::false_type{});
         __syncwarp();
         buffer ^= 1u;
     }
