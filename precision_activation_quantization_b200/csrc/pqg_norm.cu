@@ -7,6 +7,9 @@
 #include "pqg_launch.cuh"
 #include "pqg_norm.cuh"
 
+#ifndef PQG_NORM_FIRST
+#define PQG_NORM_FIRST 1
+#endif
 namespace pqg {
 namespace {
 
@@ -31,7 +34,8 @@ cudaError_t launch_norm_slots(NormParams &p, cudaStream_t stream) {
     uint32_t slots = 1;
     p.wpr = 1;
     while (p.wpr * 32u * slots < nslots) {
-        if (p.wpr < 8u) p.wpr *= 2;
+        if (slots < PQG_NORM_FIRST) slots *= 2;
+        else if (p.wpr < 8u) p.wpr *= 2;
         else slots *= 2;
     }
     if (slots == 1) return launch_norm_variant<In, KIND, 1>(p, stream);
@@ -114,6 +118,7 @@ extern "C" int pqg_rmsnorm_quant(const void *in, const void *residual, const voi
     p.scales = static_cast<uint8_t *>(scales);
     p.gscale = global_scale;
     p.eps = eps;
+    p.per_k = 1.0 / static_cast<double>(K);
     p.M = static_cast<uint32_t>(M);
     p.K = static_cast<uint32_t>(K);
     p.out_row_bytes = static_cast<uint32_t>(out_row);
