@@ -204,19 +204,6 @@ __device__ __forceinline__ void load_shared(const uint8_t *p, uint32_t (&w)[N]) 
     }
 }
 
-// 16 bytes from global to shared memory, asynchronously.
-__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void commit_copies() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-// All but the newest N groups of this thread's copies have landed.
-template <int N>
-__device__ __forceinline__ void wait_copies() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // The larger half of a pair of 16-bit numbers.
 __device__ __forceinline__ uint32_t larger_half(uint32_t v) { return max(v & 0xFFFFu, v >> 16); }
 

@@ -13,7 +13,7 @@
 #include <cstdint>
 
 #include "pqg_kernel.cuh"
-#include "pqg_norm.cuh"
+#include "pqg_memory.cuh"
 
 namespace pqg {
 

@@ -7,44 +7,48 @@
 #include "pqg_launch.cuh"
 #include "pqg_norm.cuh"
 
-#ifndef PQG_NORM_FIRST
-#define PQG_NORM_FIRST 1
-#endif
 namespace pqg {
 namespace {
 
 template <typename In, Kind KIND, int SLOTS>
-cudaError_t launch_norm_variant(const NormParams &p, cudaStream_t stream) {
+cudaError_t launch_norm_variant(const NormParams &p, int warps, cudaStream_t stream) {
     auto kernel = rmsnorm_quant_kernel<In, KIND, SLOTS>;
     int device = 0;
     cudaError_t err = cudaGetDevice(&device);
     if (err != cudaSuccess) return err;
-    static OccupancyCache cache;
-    const int bps = blocks_per_sm(cache, kernel, device, kNormThreads, 0u, 0u);
-    const int64_t rows_per_cta = (kNormThreads / 32) / p.wpr;
-    const int64_t ctas = std::min<int64_t>((p.M + rows_per_cta - 1) / rows_per_cta,
-                                           static_cast<int64_t>(sm_count(device)) * bps);
-    return launch(kernel, ctas, kNormThreads, 0, stream, p);
+    // resident blocks by warps and residual, cached per device; the shared-memory
+    // limit is that of the largest
+    static OccupancyCache cache[kNormThreads / 32];
+    const int which = p.residual != nullptr ? 1 : 0;
+    const uint32_t smem = norm_smem(SLOTS, warps, which != 0);
+    const bool cached = device >= 0 && device < kOccDevices;
+    std::atomic<int> &known = cache[warps - 1].n[cached ? device : 0][which];
+    int bps = cached ? known.load(std::memory_order_relaxed) : 0;
+    if (bps <= 0) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   static_cast<int>(norm_smem(SLOTS, kNormThreads / 32, true)));
+        if (err != cudaSuccess) return err;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&bps, kernel, warps * 32, smem) !=
+                cudaSuccess || bps < 1)
+            bps = 1;
+        if (cached) known.store(bps, std::memory_order_relaxed);
+    }
+    const int64_t ctas = std::min<int64_t>(p.M, static_cast<int64_t>(sm_count(device)) * bps);
+    return launch(kernel, ctas, warps * 32, smem, stream, p);
 }
 
 template <typename In, Kind KIND>
-cudaError_t launch_norm_slots(NormParams &p, cudaStream_t stream) {
-    // warps are added before slots: a row of 16384 elements is 8 warps x 4 slots
-    const uint32_t nslots = p.K / 16u;
-    uint32_t slots = 1;
-    p.wpr = 1;
-    while (p.wpr * 32u * slots < nslots) {
-        if (slots < PQG_NORM_FIRST) slots *= 2;
-        else if (p.wpr < 8u) p.wpr *= 2;
-        else slots *= 2;
-    }
-    if (slots == 1) return launch_norm_variant<In, KIND, 1>(p, stream);
-    if (slots == 2) return launch_norm_variant<In, KIND, 2>(p, stream);
-    return launch_norm_variant<In, KIND, 4>(p, stream);
+cudaError_t launch_norm_slots(const NormParams &p, cudaStream_t stream) {
+    // a row is units of 32 lanes x 16 elements; a warp takes 1, 2 or 4 of them, so that
+    // 8 warps are enough and as few of them as may be idle (K = 7168: 7 warps x 2)
+    const int units = static_cast<int>((p.K / 16u + 31u) / 32u);
+    if (units <= 8) return launch_norm_variant<In, KIND, 1>(p, units, stream);
+    if (units <= 16) return launch_norm_variant<In, KIND, 2>(p, (units + 1) / 2, stream);
+    return launch_norm_variant<In, KIND, 4>(p, (units + 3) / 4, stream);
 }
 
 template <typename In>
-cudaError_t launch_norm(NormParams &p, Kind kind, cudaStream_t stream) {
+cudaError_t launch_norm(const NormParams &p, Kind kind, cudaStream_t stream) {
     switch (kind) {
         case Kind::E4M3_FP32: return launch_norm_slots<In, Kind::E4M3_FP32>(p, stream);
         case Kind::E4M3_UE8M0: return launch_norm_slots<In, Kind::E4M3_UE8M0>(p, stream);
@@ -130,7 +134,6 @@ extern "C" int pqg_rmsnorm_quant(const void *in, const void *residual, const voi
     while (lanes && (1u << p.group_shift) < p.group_lanes) ++p.group_shift;
     p.mpad = static_cast<uint32_t>((M + 3) / 4 * 4);
     p.layout = static_cast<uint32_t>(scale_layout);
-    p.wpr = 1;
     const Kind kind = nvfp4                            ? Kind::E2M1_E4M3
                       : out_dtype == PQG_E2M1          ? Kind::E2M1_UE8M0
                       : scale_fmt == PQG_SCALE_UE8M0 ? Kind::E4M3_UE8M0

@@ -21,6 +21,7 @@
 #include <cstdint>
 
 #include "pqg_kernel.cuh"
+#include "pqg_memory.cuh"
 
 namespace pqg {
 
@@ -42,10 +43,9 @@ struct NormParams {
     uint32_t group_shift;      // log2(group_lanes)
     uint32_t mpad;
     uint32_t layout;
-    uint32_t wpr;              // warps per row: 1, 2, 4 or 8
 };
 
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 256;      // of a block, at most: 1 to 8 warps share a row
 
 // 32-byte load that stays in L1: the weights, which every row reads again.
 __device__ __forceinline__ void load32B_cached(const void *p, uint32_t (&r)[8]) {
@@ -54,28 +54,16 @@ __device__ __forceinline__ void load32B_cached(const void *p, uint32_t (&r)[8]) 
                    "=r"(r[6]), "=r"(r[7])
                  : "l"(p));
 }
-// Plain (coherent) 32-byte load: the residual may be updated in place.
-__device__ __forceinline__ void load32B_coherent(const void *p, uint32_t (&r)[8]) {
-    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7])
-                 : "l"(p)
-                 : "memory");
-}
-__device__ __forceinline__ void store32B(void *p, const uint32_t (&r)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-
-// Two fp32 values rounded to the 16-bit type (nearest even), `lo` in the low half.
+// x + r for two packed pairs, each sum rounded once to the type.  (One rounding to
+// fp32 and one to the type give the same: where the fp32 sum is not exact the
+// smaller term is below 2^-13 of the larger, less than half a step of the type.)
 template <typename T>
-__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
     uint32_t r;
     if constexpr (std::is_same<T, __nv_bfloat16>::value)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     else
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
 
@@ -136,52 +124,81 @@ __device__ __forceinline__ void store_norm_scale(const NormParams &p, uint32_t r
     }
 }
 
-// A row is shared by p.wpr warps; a thread holds SLOTS slots of 16 consecutive
+// A row is shared by the block's warps; a thread holds SLOTS slots of 16 consecutive
 // elements, neighbouring lanes holding neighbouring slots, so that a group is
 // 1 to 8 neighbouring lanes (or, per token, the whole row).
-#ifndef PQG_NORM_OCC
-#define PQG_NORM_OCC 0
-#endif
+//
+// Shared memory: [2 buffers][SLOTS][x, r][warp][1 KB], x alone without a residual.
+__host__ __device__ constexpr uint32_t norm_smem(int slots, int warps, bool residual) {
+    return 2u * slots * (residual ? 2u : 1u) * warps * 1024u;
+}
+
 template <typename In, Kind KIND, int SLOTS>
-__global__ void __launch_bounds__(kNormThreads, SLOTS == 2 ? PQG_NORM_OCC : 0)
+__global__ void __launch_bounds__(kNormThreads)
     rmsnorm_quant_kernel(const __grid_constant__ NormParams p) {
+    extern __shared__ __align__(128) uint8_t rows[];
     __shared__ double sums[2][kNormThreads / 32];
     __shared__ float maxima[2][kNormThreads / 32];
     __shared__ float nv[KIND == Kind::E2M1_E4M3 ? kNvTable : 1];
 
     wait_for_producer();                        // before the first global access
     if constexpr (KIND == Kind::E2M1_E4M3) {
-        Params q;
-        q.gscale = p.gscale;
-        build_nvfp4_table(q, nv);
+        // build_nvfp4_table for a block of any size
+        const float g = __ldg(p.gscale);
+        for (uint32_t c = threadIdx.x; c < 128u; c += blockDim.x) {
+            const float d = e4m3_code_value(c);
+            nv[c] = d == 0.0f ? 0.0f : __fdiv_rn(g, d);
+        }
+        if (threadIdx.x == 0u) nv[128] = g;
+        __syncthreads();
     }
     const uint32_t lane = threadIdx.x & 31u;
     const uint32_t warp = threadIdx.x >> 5;
-    const uint32_t wpr = p.wpr;
-    const uint32_t rows_per_iter = (kNormThreads / 32) / wpr;
-    const uint32_t sub = warp / wpr;            // this warp's row within the iteration
-    const uint32_t tpr = wpr * 32u;
-    const uint32_t tid = threadIdx.x - sub * tpr;   // thread index within the row
+    const uint32_t tid = threadIdx.x, tpr = blockDim.x, warps = blockDim.x >> 5;
     const uint32_t nslots = p.K / 16u;
     const uint64_t row_bytes = static_cast<uint64_t>(p.K) * 2u;
 
-    uint32_t parity = 0;
-    for (uint32_t base = blockIdx.x * rows_per_iter; base < p.M;
-         base += gridDim.x * rows_per_iter, parity ^= 1u) {
-        const uint32_t row = base + sub;        // warp-uniform
-        const bool live = row < p.M;
-
-        // this warp's share of the row it takes next, into L2
-        {
-            const uint32_t next = row + gridDim.x * rows_per_iter;
-            const uint32_t part = ((p.K * 2u / wpr) + 15u) & ~15u;
-            const uint32_t from = (warp - sub * wpr) * part;
-            if (lane == 0u && next < p.M && from < p.K * 2u) {
-                const uint32_t n = min(part, p.K * 2u - from);
-                prefetch_l2(p.in + next * row_bytes + from, n);
-                if (p.residual != nullptr) prefetch_l2(p.residual + next * row_bytes + from, n);
+    const uint32_t inputs = p.residual != nullptr ? 2u : 1u;
+    const uint32_t rows_at = static_cast<uint32_t>(__cvta_generic_to_shared(rows)) + warp * 1024u;
+    const uint32_t part = tpr * 32u;                    // bytes of one slot of all threads
+    const uint32_t buffer_bytes = SLOTS * inputs * part;
+    // Part c (16 bytes) of a warp's 1 KB goes to place c ^ ((c >> 3) & 1): lanes copy
+    // neighbouring parts, then read parts 2 lane and 2 lane + 1, both without conflicts.
+    const uint32_t place = (lane ^ ((lane >> 3) & 1u)) * 16u;
+    const uint32_t flip = (lane >> 2) & 1u;             // of parts 2 lane and 2 lane + 1
+    auto copy_row = [&](uint32_t row, uint32_t buffer) {
+        if (row < p.M) {
+#pragma unroll
+            for (int j = 0; j < SLOTS; ++j) {
+                const uint32_t slot = (tid & ~31u) + j * tpr;   // the warp's first
+                const uint64_t from = row * row_bytes + slot * 32u + lane * 16u;
+                const uint32_t to = rows_at + buffer * buffer_bytes + j * inputs * part + place;
+#pragma unroll
+                for (uint32_t half = 0; half < 2; ++half) {
+                    if (slot + half * 16u + lane / 2u >= nslots) continue;
+                    copy16(to + half * 512u, p.in + from + half * 512u);
+                    if (inputs == 2u)
+                        copy16(to + part + half * 512u, p.residual + from + half * 512u);
+                }
             }
         }
+        commit_copies();
+    };
+    auto read_slot = [&](uint32_t at, uint32_t (&v)[8]) {
+        const uint8_t *mine = rows + at + warp * 1024u + lane * 32u;
+        const uint4 a = *reinterpret_cast<const uint4 *>(mine + flip * 16u);
+        const uint4 b = *reinterpret_cast<const uint4 *>(mine + (flip ^ 1u) * 16u);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    };
+
+    uint32_t parity = 0;
+    copy_row(blockIdx.x, 0u);
+    for (uint32_t row = blockIdx.x; row < p.M; row += gridDim.x, parity ^= 1u) {
+        copy_row(row + gridDim.x, parity ^ 1u);
+        wait_copies<1>();
+        __syncwarp();
+
         // -- h = x + r, and this thread's share of its sum of squares -----------
         uint32_t h[SLOTS][8];
         double ss = 0.0;
@@ -190,23 +207,17 @@ __global__ void __launch_bounds__(kNormThreads, SLOTS == 2 ? PQG_NORM_OCC : 0)
             const uint32_t slot = tid + j * tpr;
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[j][i] = 0u;
-            if (live && slot < nslots) {
-                const uint64_t at = row * row_bytes + slot * 32u;
-                load32B_coherent(p.in + at, h[j]);
-                if (p.residual != nullptr) {
+            if (slot < nslots) {
+                const uint32_t at = parity * buffer_bytes + j * inputs * part;
+                read_slot(at, h[j]);
+                if (inputs == 2u) {
                     uint32_t r[8];
-                    load32B_coherent(p.residual + at, r);
+                    read_slot(at + part, r);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float a0, a1, b0, b1;
-                        widen2<In>(h[j][i], a0, a1);
-                        widen2<In>(r[i], b0, b1);
-                        const float2 sum = __fadd2_rn(make_float2(a0, a1), make_float2(b0, b1));
-                        h[j][i] = narrow2<In>(sum.x, sum.y);
-                    }
+                    for (int i = 0; i < 8; ++i) h[j][i] = add2<In>(h[j][i], r[i]);
                 }
                 if (p.residual_out != nullptr)
-                    store32B(p.residual_out + at, h[j]);
+                    store32B(p.residual_out + row * row_bytes + slot * 32u, h[j]);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -216,13 +227,14 @@ __global__ void __launch_bounds__(kNormThreads, SLOTS == 2 ? PQG_NORM_OCC : 0)
                 ss = fma(static_cast<double>(a1), static_cast<double>(a1), ss);
             }
         }
+        // (the shuffles also order the warp's reads before the copies into this buffer)
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if (wpr > 1) {
+        if (warps > 1u) {
             if (lane == 0) sums[parity][warp] = ss;
-            asm volatile("bar.sync %0, %1;" ::"r"(1u + sub), "r"(wpr * 32u) : "memory");
+            __syncthreads();
             ss = 0.0;
-            for (uint32_t w = 0; w < wpr; ++w) ss += sums[parity][sub * wpr + w];
+            for (uint32_t w = 0; w < warps; ++w) ss += sums[parity][w];
         }
         const float inv = inverse_root(fma(ss, p.per_k, p.eps));
 
@@ -248,17 +260,16 @@ __global__ void __launch_bounds__(kNormThreads, SLOTS == 2 ? PQG_NORM_OCC : 0)
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1)
                 row_max = fmaxf(row_max, __shfl_xor_sync(0xFFFFFFFFu, row_max, o));
-            if (wpr > 1) {
+            if (warps > 1u) {
                 if (lane == 0) maxima[parity][warp] = row_max;
-                asm volatile("bar.sync %0, %1;" ::"r"(1u + sub), "r"(wpr * 32u) : "memory");
-                for (uint32_t w = 0; w < wpr; ++w)
-                    row_max = fmaxf(row_max, maxima[parity][sub * wpr + w]);
+                __syncthreads();
+                for (uint32_t w = 0; w < warps; ++w) row_max = fmaxf(row_max, maxima[parity][w]);
             }
         }
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
             const uint32_t slot = tid + j * tpr;
-            const bool ok = live && slot < nslots;
+            const bool ok = slot < nslots;
             float y[16];
             uint32_t w[8];
 #pragma unroll
