@@ -10,9 +10,9 @@
 namespace pqg {
 namespace {
 
-template <typename In, Kind KIND, int SLOTS>
+template <typename In, Kind KIND, int SLOTS, bool PER_TOKEN>
 cudaError_t launch_norm_variant(const NormParams &p, int warps, cudaStream_t stream) {
-    auto kernel = rmsnorm_quant_kernel<In, KIND, SLOTS>;
+    auto kernel = rmsnorm_quant_kernel<In, KIND, SLOTS, PER_TOKEN>;
     int device = 0;
     cudaError_t err = cudaGetDevice(&device);
     if (err != cudaSuccess) return err;
@@ -37,24 +37,32 @@ cudaError_t launch_norm_variant(const NormParams &p, int warps, cudaStream_t str
     return launch(kernel, ctas, warps * 32, smem, stream, p);
 }
 
-template <typename In, Kind KIND>
+template <typename In, Kind KIND, bool PER_TOKEN>
 cudaError_t launch_norm_slots(const NormParams &p, cudaStream_t stream) {
     // a row is units of 32 lanes x 16 elements; a warp takes 1, 2 or 4 of them, so that
     // 8 warps are enough and as few of them as may be idle (K = 7168: 7 warps x 2)
     const int units = static_cast<int>((p.K / 16u + 31u) / 32u);
-    if (units <= 8) return launch_norm_variant<In, KIND, 1>(p, units, stream);
-    if (units <= 16) return launch_norm_variant<In, KIND, 2>(p, (units + 1) / 2, stream);
-    return launch_norm_variant<In, KIND, 4>(p, (units + 3) / 4, stream);
+    if (units <= 8) return launch_norm_variant<In, KIND, 1, PER_TOKEN>(p, units, stream);
+    if (units <= 16)
+        return launch_norm_variant<In, KIND, 2, PER_TOKEN>(p, (units + 1) / 2, stream);
+    return launch_norm_variant<In, KIND, 4, PER_TOKEN>(p, (units + 3) / 4, stream);
+}
+
+template <typename In, Kind KIND>
+cudaError_t launch_norm_kind(const NormParams &p, cudaStream_t stream) {
+    if constexpr (!is_e2m1(KIND))   // FP4 codes have groups of 16 to 128
+        if (p.group_lanes == 0u) return launch_norm_slots<In, KIND, true>(p, stream);
+    return launch_norm_slots<In, KIND, false>(p, stream);
 }
 
 template <typename In>
 cudaError_t launch_norm(const NormParams &p, Kind kind, cudaStream_t stream) {
     switch (kind) {
-        case Kind::E4M3_FP32: return launch_norm_slots<In, Kind::E4M3_FP32>(p, stream);
-        case Kind::E4M3_UE8M0: return launch_norm_slots<In, Kind::E4M3_UE8M0>(p, stream);
-        case Kind::INT8_FP32: return launch_norm_slots<In, Kind::INT8_FP32>(p, stream);
-        case Kind::E2M1_UE8M0: return launch_norm_slots<In, Kind::E2M1_UE8M0>(p, stream);
-        case Kind::E2M1_E4M3: return launch_norm_slots<In, Kind::E2M1_E4M3>(p, stream);
+        case Kind::E4M3_FP32: return launch_norm_kind<In, Kind::E4M3_FP32>(p, stream);
+        case Kind::E4M3_UE8M0: return launch_norm_kind<In, Kind::E4M3_UE8M0>(p, stream);
+        case Kind::INT8_FP32: return launch_norm_kind<In, Kind::INT8_FP32>(p, stream);
+        case Kind::E2M1_UE8M0: return launch_norm_kind<In, Kind::E2M1_UE8M0>(p, stream);
+        case Kind::E2M1_E4M3: return launch_norm_kind<In, Kind::E2M1_E4M3>(p, stream);
     }
     return cudaErrorInvalidValue;
 }
@@ -127,7 +135,7 @@ extern "C" int pqg_rmsnorm_quant(const void *in, const void *residual, const voi
     p.K = static_cast<uint32_t>(K);
     p.out_row_bytes = static_cast<uint32_t>(out_row);
     p.ng = static_cast<uint32_t>(K / group);
-    // a group of 16, 32, 64 or 128 is 1, 2, 4 or 8 lanes; any other is the row
+    // a group of 16, 32, 64 or 128 is 1, 2, 4 or 8 lanes; any other is the row (0)
     const bool lanes = group == 16 || group == 32 || group == 64 || group == 128;
     p.group_lanes = lanes ? static_cast<uint32_t>(group) / 16u : 0u;
     p.group_shift = 0;

@@ -39,7 +39,7 @@ struct NormParams {
     uint32_t K;
     uint32_t out_row_bytes;
     uint32_t ng;               // groups per row
-    uint32_t group_lanes;      // 16-element slots per group: 1, 2, 4, 8; 0: the whole row
+    uint32_t group_lanes;      // 16-element slots per group: 1, 2, 4, 8 (not per token)
     uint32_t group_shift;      // log2(group_lanes)
     uint32_t mpad;
     uint32_t layout;
@@ -128,17 +128,17 @@ __device__ __forceinline__ void store_norm_scale(const NormParams &p, uint32_t r
 // elements, neighbouring lanes holding neighbouring slots, so that a group is
 // 1 to 8 neighbouring lanes (or, per token, the whole row).
 //
-// Shared memory: [2 buffers][SLOTS][x, r][warp][1 KB], x alone without a residual.
+// Shared memory: [SLOTS][x, r][warp][1 KB], x alone without a residual.
 __host__ __device__ constexpr uint32_t norm_smem(int slots, int warps, bool residual) {
-    return 2u * slots * (residual ? 2u : 1u) * warps * 1024u;
+    return slots * (residual ? 2u : 1u) * warps * 1024u;
 }
 
-template <typename In, Kind KIND, int SLOTS>
+template <typename In, Kind KIND, int SLOTS, bool PER_TOKEN>
 __global__ void __launch_bounds__(kNormThreads)
     rmsnorm_quant_kernel(const __grid_constant__ NormParams p) {
     extern __shared__ __align__(128) uint8_t rows[];
     __shared__ double sums[2][kNormThreads / 32];
-    __shared__ float maxima[2][kNormThreads / 32];
+    __shared__ float maxima[PER_TOKEN ? 2 : 1][kNormThreads / 32];
     __shared__ float nv[KIND == Kind::E2M1_E4M3 ? kNvTable : 1];
 
     wait_for_producer();                        // before the first global access
@@ -161,18 +161,17 @@ __global__ void __launch_bounds__(kNormThreads)
     const uint32_t inputs = p.residual != nullptr ? 2u : 1u;
     const uint32_t rows_at = static_cast<uint32_t>(__cvta_generic_to_shared(rows)) + warp * 1024u;
     const uint32_t part = tpr * 32u;                    // bytes of one slot of all threads
-    const uint32_t buffer_bytes = SLOTS * inputs * part;
     // Part c (16 bytes) of a warp's 1 KB goes to place c ^ ((c >> 3) & 1): lanes copy
     // neighbouring parts, then read parts 2 lane and 2 lane + 1, both without conflicts.
     const uint32_t place = (lane ^ ((lane >> 3) & 1u)) * 16u;
     const uint32_t flip = (lane >> 2) & 1u;             // of parts 2 lane and 2 lane + 1
-    auto copy_row = [&](uint32_t row, uint32_t buffer) {
+    auto copy_row = [&](uint32_t row) {
         if (row < p.M) {
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
                 const uint32_t slot = (tid & ~31u) + j * tpr;   // the warp's first
                 const uint64_t from = row * row_bytes + slot * 32u + lane * 16u;
-                const uint32_t to = rows_at + buffer * buffer_bytes + j * inputs * part + place;
+                const uint32_t to = rows_at + j * inputs * part + place;
 #pragma unroll
                 for (uint32_t half = 0; half < 2; ++half) {
                     if (slot + half * 16u + lane / 2u >= nslots) continue;
@@ -193,22 +192,20 @@ __global__ void __launch_bounds__(kNormThreads)
     };
 
     uint32_t parity = 0;
-    copy_row(blockIdx.x, 0u);
+    copy_row(blockIdx.x);
     for (uint32_t row = blockIdx.x; row < p.M; row += gridDim.x, parity ^= 1u) {
-        copy_row(row + gridDim.x, parity ^ 1u);
-        wait_copies<1>();
+        wait_copies<0>();
         __syncwarp();
 
-        // -- h = x + r, and this thread's share of its sum of squares -----------
+        // -- h = x + r; the next row's copies start as soon as the buffer is read ------
         uint32_t h[SLOTS][8];
-        double ss = 0.0;
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
             const uint32_t slot = tid + j * tpr;
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[j][i] = 0u;
             if (slot < nslots) {
-                const uint32_t at = parity * buffer_bytes + j * inputs * part;
+                const uint32_t at = j * inputs * part;
                 read_slot(at, h[j]);
                 if (inputs == 2u) {
                     uint32_t r[8];
@@ -219,6 +216,12 @@ __global__ void __launch_bounds__(kNormThreads)
                 if (p.residual_out != nullptr)
                     store32B(p.residual_out + row * row_bytes + slot * 32u, h[j]);
             }
+        }
+        __syncwarp();                           // the warp has read its buffer
+        copy_row(row + gridDim.x);
+        double ss = 0.0;
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 float a0, a1;
@@ -227,7 +230,6 @@ __global__ void __launch_bounds__(kNormThreads)
                 ss = fma(static_cast<double>(a1), static_cast<double>(a1), ss);
             }
         }
-        // (the shuffles also order the warp's reads before the copies into this buffer)
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
         if (warps > 1u) {
@@ -239,23 +241,29 @@ __global__ void __launch_bounds__(kNormThreads)
         const float inv = inverse_root(fma(ss, p.per_k, p.eps));
 
         // -- y, its groups' absmax, scales and codes ------------------------------
-        float row_max = 0.0f;                   // per token: over the whole row
-        if (p.group_lanes == 0u) {
+        auto norm_slot = [&](int j, uint32_t slot, float (&y)[16]) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = 0u;
+            if (slot < nslots) load32B_cached(p.weight + slot * 32u, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float a0, a1, w0, w1;
+                widen2<In>(h[j][i], a0, a1);
+                widen2<In>(w[i], w0, w1);
+                const float2 v = __fmul2_rn(
+                    __fmul2_rn(make_float2(a0, a1), make_float2(inv, inv)), make_float2(w0, w1));
+                y[2 * i] = v.x;
+                y[2 * i + 1] = v.y;
+            }
+        };
+        // per token: the whole row's absmax first, y kept in registers
+        float kept[PER_TOKEN ? SLOTS : 1][16], row_max = 0.0f;
+        if constexpr (PER_TOKEN) {
 #pragma unroll
             for (int j = 0; j < SLOTS; ++j) {
-                const uint32_t slot = tid + j * tpr;
-                if (slot >= nslots) continue;
-                uint32_t w[8];
-                load32B_cached(p.weight + slot * 32u, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float a0, a1, w0, w1;
-                    widen2<In>(h[j][i], a0, a1);
-                    widen2<In>(w[i], w0, w1);
-                    const float2 v = __fmul2_rn(
-                        __fmul2_rn(make_float2(a0, a1), make_float2(inv, inv)), make_float2(w0, w1));
-                    row_max = fmaxf(row_max, fmaxf(fabsf(v.x), fabsf(v.y)));
-                }
+                norm_slot(j, tid + j * tpr, kept[j]);
+                row_max = fmaxf(row_max, absmax16(kept[j]));
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1)
@@ -271,22 +279,12 @@ __global__ void __launch_bounds__(kNormThreads)
             const uint32_t slot = tid + j * tpr;
             const bool ok = slot < nslots;
             float y[16];
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = 0u;
-            if (ok) load32B_cached(p.weight + slot * 32u, w);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float a0, a1, w0, w1;
-                widen2<In>(h[j][i], a0, a1);
-                widen2<In>(w[i], w0, w1);
-                const float2 v = __fmul2_rn(
-                    __fmul2_rn(make_float2(a0, a1), make_float2(inv, inv)), make_float2(w0, w1));
-                y[2 * i] = v.x;
-                y[2 * i + 1] = v.y;
-            }
             float amax = row_max;
-            if (p.group_lanes != 0u) {
+            if constexpr (PER_TOKEN) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = kept[j][i];
+            } else {
+                norm_slot(j, slot, y);
                 amax = absmax16(y);
                 for (uint32_t o = 1; o < p.group_lanes; o <<= 1)
                     amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
@@ -297,9 +295,9 @@ __global__ void __launch_bounds__(kNormThreads)
             // quotient is proved for 16-bit inputs only
             encode16<KIND, 2>(y, gs, code);
 
-            const uint32_t g = p.group_lanes == 0u ? 0u : slot >> p.group_shift;
+            const uint32_t g = PER_TOKEN ? 0u : slot >> p.group_shift;
             uint32_t word = gs.e8;              // per token: bytes 1..3 are 0
-            if (p.layout == kPacked && p.group_lanes != 0u) {
+            if (!PER_TOKEN && p.layout == kPacked) {
                 // exponents of groups 4j..4j+3, from the 4 groups' lanes
                 word = ok ? gs.e8 << (8u * (g & 3u)) : 0u;
                 word |= __shfl_xor_sync(0xFFFFFFFFu, word, p.group_lanes);
@@ -311,8 +309,7 @@ __global__ void __launch_bounds__(kNormThreads)
                 store8B(dst + slot * 8u, code[0], code[1]);
             else
                 store16B(dst + slot * 16u, code[0], code[1], code[2], code[3]);
-            const bool first = p.group_lanes == 0u ? tid == 0u && j == 0
-                                                   : (slot & (p.group_lanes - 1u)) == 0u;
+            const bool first = PER_TOKEN ? slot == 0u : (slot & (p.group_lanes - 1u)) == 0u;
             if (first) store_norm_scale<KIND>(p, row, g, gs, word);
         }
     }
