@@ -4,6 +4,8 @@
 
 namespace pqg {
 
+void segs_divider(uint32_t segs, uint32_t *magic, uint32_t *shift);   // pqg_api.cu
+
 int check_cache(const pqg_kv_cache *cache, CacheView *view) {
     if (cache == nullptr) return PQG_ERR_INVALID_ARG;
     if (cache->format != PQG_KV_MXFP4 && cache->format != PQG_KV_NVFP4) return PQG_ERR_INVALID_ARG;
@@ -30,6 +32,7 @@ int check_cache(const pqg_kv_cache *cache, CacheView *view) {
     view->num_pages = static_cast<uint32_t>(cache->num_pages);
     view->heads = static_cast<uint32_t>(cache->kv_heads);
     view->head_dim = static_cast<uint32_t>(D);
+    segs_divider(view->heads, &view->heads_magic, &view->heads_shift);
     view->page_shift = 4;
     while ((1 << view->page_shift) < P) ++view->page_shift;
     // the four buffers, and the global scales, lie apart
@@ -74,7 +77,7 @@ int pqg_kv_write(const pqg_kv_cache *cache, const void *k, const void *v, const 
     const uint32_t tokens_per_warp = 32u / (p.c.head_dim / 16u);
     const int64_t warps = (T + tokens_per_warp - 1) / tokens_per_warp * cache->kv_heads;
     const int64_t blocks = (warps * 32 + kCacheThreads - 1) / kCacheThreads;
-    if (blocks >= (int64_t{1} << 31)) return PQG_ERR_INVALID_ARG;
+    if (warps > (int64_t{1} << 31) - kCacheThreads) return PQG_ERR_INVALID_ARG;
     if (T == 0) return PQG_OK;
     if (k == nullptr || v == nullptr || slots == nullptr) return PQG_ERR_INVALID_ARG;
     if (!aligned(k, 32) || !aligned(v, 32) || !aligned(slots, 4) || k_stride % 16 != 0 ||
@@ -109,9 +112,9 @@ int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table, int64_t ta
     if (ts != PQG_OK) return ts;
     const int64_t row = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
     if (M < 0 || M >= (int64_t{1} << 31)) return PQG_ERR_INVALID_ARG;
-    const int64_t blocks = (M * cache->kv_heads * (cache->head_dim / 16) + kCacheThreads - 1) /
-                           kCacheThreads;
-    if (blocks >= (int64_t{1} << 31)) return PQG_ERR_INVALID_ARG;
+    const int64_t rowheads = (M + kReadRows - 1) / kReadRows * cache->kv_heads;
+    const int64_t blocks = (rowheads * (cache->head_dim / 16) + kCacheThreads - 1) / kCacheThreads;
+    if (rowheads > (int64_t{1} << 31) - kCacheThreads) return PQG_ERR_INVALID_ARG;
     if (M == 0 || B == 0) return PQG_OK;
     if (page_table == nullptr || indptr == nullptr || k_out == nullptr || v_out == nullptr)
         return PQG_ERR_INVALID_ARG;

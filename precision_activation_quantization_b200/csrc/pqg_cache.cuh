@@ -25,7 +25,13 @@ struct CacheView {
     uint32_t page_shift;       // log2(page size)
     uint32_t heads;
     uint32_t head_dim;
+    uint32_t heads_magic;      // x / heads = umulhi(x, heads_magic) >> heads_shift for
+    uint32_t heads_shift;      // x < 2^31 (div_segs' rule; magic 0: one head)
 };
+
+__device__ __forceinline__ uint32_t div_heads(const CacheView &c, uint32_t x) {
+    return c.heads_magic == 0u ? x : __umulhi(x, c.heads_magic) >> c.heads_shift;
+}
 
 // First byte of the codes of (page, head, offset) and of the scale bytes of
 // (page, head, group 0, offset); 64-bit: a cache passes 4 GB.
@@ -66,22 +72,23 @@ __global__ void __launch_bounds__(kCacheThreads)
     const uint32_t rpw = 32u / lanes;           // tokens per warp
     const uint32_t lane = threadIdx.x & 31u;
     const uint32_t sub = lane / lanes, col = (lane - sub * lanes) * 16u;
-    const uint64_t warp = (static_cast<uint64_t>(blockIdx.x) * kCacheThreads + threadIdx.x) >> 5;
-    const uint32_t head = static_cast<uint32_t>(warp % p.c.heads);
-    const uint64_t token = warp / p.c.heads * rpw + sub;
+    const uint32_t warp = blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t block = div_heads(p.c, warp), head = warp - block * p.c.heads;
+    const uint64_t token = static_cast<uint64_t>(block) * rpw + sub;
+    // the rows are loaded while the slot is in flight: a padding token's row is read too
+    const bool some = token < p.T;
     int slot = -1;
-    if (token < p.T) slot = __ldg(p.slots + token);
-    const bool live = slot >= 0 && (static_cast<uint32_t>(slot) >> p.c.page_shift) < p.c.num_pages;
-
+    if (some) slot = __ldg(p.slots + token);
     uint32_t x[2][8];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[n][i] = 0u;
-        if (live)
+        if (some)
             load32B(p.src[n] + token * p.stride[n] +
                         (static_cast<uint64_t>(head) * p.c.head_dim + col) * 2u, x[n]);
     }
+    const bool live = slot >= 0 && (static_cast<uint32_t>(slot) >> p.c.page_shift) < p.c.num_pages;
     const uint32_t page = static_cast<uint32_t>(slot) >> p.c.page_shift;
     const uint32_t off = static_cast<uint32_t>(slot) & ((1u << p.c.page_shift) - 1u);
 #pragma unroll
@@ -140,21 +147,25 @@ __device__ __forceinline__ int find_sequence(const int32_t *indptr, uint32_t B, 
     return *first <= row && row < __ldg(indptr + lo + 1) ? static_cast<int>(lo) : -1;
 }
 
-// The four fp32 values of codes in 16 bits of a packed word, times `s`, then
-// rounded to 16 bits: two packed words.
-template <typename Out>
-__device__ __forceinline__ void decode4(uint32_t codes, float s, float inv, uint32_t (&w)[2]) {
-    uint32_t a, b;
-    asm("{\n\t.reg .b8 p, q, t0, t1;\n\t"
-        "mov.b32 {p, q, t0, t1}, %2;\n\t"
+// Eight codes of a packed word, times `s` (and, NVFP4, `inv`), each rounded once to
+// 16 bits: four packed words.  code * scale is exact in fp32.
+template <typename Out, bool INV>
+__device__ __forceinline__ void decode8(uint32_t codes, float s, float inv, uint32_t *w) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 p, q, s, t;\n\t"
+        "mov.b32 {p, q, s, t}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, p;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %1, q;\n\t}"
-        : "=r"(a), "=r"(b) : "r"(codes));
-    const float2 lo = __half22float2(*reinterpret_cast<__half2 *>(&a));
-    const float2 hi = __half22float2(*reinterpret_cast<__half2 *>(&b));
-    // code * scale is exact in fp32; MXFP4's inv is 1
-    w[0] = narrow2<Out>(__fmul_rn(lo.x * s, inv), __fmul_rn(lo.y * s, inv));
-    w[1] = narrow2<Out>(__fmul_rn(hi.x * s, inv), __fmul_rn(hi.y * s, inv));
+        "cvt.rn.f16x2.e2m1x2 %1, q;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, s;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, t;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(codes));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float2 v = __fmul2_rn(__half22float2(*reinterpret_cast<__half2 *>(&h[i])),
+                              make_float2(s, s));
+        if constexpr (INV) v = __fmul2_rn(v, make_float2(inv, inv));
+        w[i] = narrow2<Out>(v.x, v.y);
+    }
 }
 
 // 2^(e - 127) for a UE8M0 byte (e = 0: 2^-127, a subnormal).
@@ -162,51 +173,73 @@ __device__ __forceinline__ float ue8m0_value(uint32_t e) {
     return e == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(e << 23);
 }
 
-// One lane decodes 16 elements of a key row and of the value row.  Bound by the
-// 16-bit output.
+// One lane decodes 16 elements of the key rows and of the value rows of kReadRows
+// neighbouring output rows, so that finding the sequence and the page is shared
+// and eight loads of codes are in flight.  Bound by the 16-bit output.
+constexpr uint32_t kReadRows = 4;
+
 template <typename Out, int G>
 __global__ void __launch_bounds__(kCacheThreads)
     kv_read_kernel(const __grid_constant__ ReadParams p) {
     wait_for_producer();
-    const uint32_t lanes = p.c.head_dim / 16u;
+    const uint32_t lane_shift = p.c.head_dim == 64u ? 2u : p.c.head_dim == 128u ? 3u : 4u;
     const uint64_t unit = static_cast<uint64_t>(blockIdx.x) * kCacheThreads + threadIdx.x;
-    const uint64_t rowhead = unit / lanes;
-    const uint32_t col = static_cast<uint32_t>(unit - rowhead * lanes) * 16u;
-    const uint64_t row64 = rowhead / p.c.heads;
-    const uint32_t head = static_cast<uint32_t>(rowhead - row64 * p.c.heads);
-    if (row64 < p.M) {
-        const uint32_t row = static_cast<uint32_t>(row64);
-        int first;
-        const int b = find_sequence(p.indptr, p.B, static_cast<int>(row), &first);
-        const uint32_t j = row - static_cast<uint32_t>(first);
-        if (b >= 0 && (j >> p.c.page_shift) < p.max_pages) {
-            const int page = __ldg(p.table + static_cast<uint64_t>(b) * p.table_stride +
-                                   (j >> p.c.page_shift));
-            const bool good = page >= 0 && static_cast<uint32_t>(page) < p.c.num_pages;
-            const uint32_t off = j & ((1u << p.c.page_shift) - 1u);
+    const uint32_t col = (static_cast<uint32_t>(unit) & ((1u << lane_shift) - 1u)) * 16u;
+    const uint32_t rowhead = static_cast<uint32_t>(unit >> lane_shift);   // < 2^31
+    const uint32_t group = div_heads(p.c, rowhead), head = rowhead - group * p.c.heads;
+    const uint64_t row0 = static_cast<uint64_t>(group) * kReadRows;
+    if (row0 < p.M) {
+        const float inv[2] = {G == 16 ? __frcp_rn(__ldg(p.c.gscale)) : 1.0f,
+                              G == 16 ? __frcp_rn(__ldg(p.c.gscale + 1)) : 1.0f};
+        uint2 codes[kReadRows][2];
+        uint32_t scale[kReadRows][2];
+        bool held[kReadRows], good[kReadRows];
+        int b = -1, first = 0, last = INT32_MIN;    // the sequence and its rows [first, last)
+#pragma unroll
+        for (uint32_t i = 0; i < kReadRows; ++i) {
+            const uint64_t row = row0 + i;
+            held[i] = good[i] = false;
+            if (row < p.M) {
+                if (i == 0u || static_cast<int>(row) >= last) {
+                    b = find_sequence(p.indptr, p.B, static_cast<int>(row), &first);
+                    last = b >= 0 ? __ldg(p.indptr + b + 1) : static_cast<int>(row) + 1;
+                }
+                const uint32_t j = static_cast<uint32_t>(row) - static_cast<uint32_t>(first);
+                held[i] = b >= 0 && (j >> p.c.page_shift) < p.max_pages;
+                if (held[i]) {
+                    const int page = __ldg(p.table + static_cast<uint64_t>(b) * p.table_stride +
+                                           (j >> p.c.page_shift));
+                    good[i] = static_cast<uint32_t>(page) < p.c.num_pages;
+                    if (good[i]) {
+                        const uint32_t off = j & ((1u << p.c.page_shift) - 1u);
+                        const uint64_t at = code_offset(p.c, page, head, off) + col / 2u;
+                        const uint64_t sc = scale_offset<G>(p.c, page, head, col / G, off);
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            codes[i][n] =
+                                __ldg(reinterpret_cast<const uint2 *>(p.c.codes[n] + at));
+                            scale[i][n] = __ldg(p.c.scales[n] + sc);
+                        }
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kReadRows; ++i) {
+            if (!held[i]) continue;
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 uint32_t w[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = 0u;
-                if (good) {
-                    const uint32_t pg = static_cast<uint32_t>(page);
-                    const uint2 codes = *reinterpret_cast<const uint2 *>(
-                        p.c.codes[n] + code_offset(p.c, pg, head, off) + col / 2u);
-                    const uint32_t e =
-                        p.c.scales[n][scale_offset<G>(p.c, pg, head, col / G, off)];
-                    const float s = G == 16 ? e4m3_code_value(e & 0x7Fu) : ue8m0_value(e);
-                    const float inv = G == 16 ? __frcp_rn(__ldg(p.c.gscale + n)) : 1.0f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t two[2];
-                        decode4<Out>((i < 2 ? codes.x : codes.y) >> (16 * (i & 1)), s, inv, two);
-                        w[2 * i] = two[0];
-                        w[2 * i + 1] = two[1];
-                    }
+                for (int k = 0; k < 8; ++k) w[k] = 0u;
+                if (good[i]) {
+                    const float s = G == 16 ? e4m3_code_value(scale[i][n] & 0x7Fu)
+                                            : ue8m0_value(scale[i][n]);
+                    decode8<Out, G == 16>(codes[i][n].x, s, inv[n], w);
+                    decode8<Out, G == 16>(codes[i][n].y, s, inv[n], w + 4);
                 }
-                store32B(p.dst[n] + ((static_cast<uint64_t>(row) * p.c.heads + head) *
-                                         p.c.head_dim + col) * 2u, w);
+                store32B(p.dst[n] + (((row0 + i) * p.c.heads + head) * p.c.head_dim + col) * 2u,
+                         w);
             }
         }
     }

@@ -10,6 +10,8 @@
 namespace pqg {
 namespace {
 
+constexpr uint32_t kManyRows = 1024;
+
 template <typename In, Kind KIND, int SLOTS, bool PER_TOKEN>
 cudaError_t launch_norm_variant(const NormParams &p, int warps, cudaStream_t stream) {
     auto kernel = rmsnorm_quant_kernel<In, KIND, SLOTS, PER_TOKEN>;
@@ -42,6 +44,11 @@ cudaError_t launch_norm_slots(const NormParams &p, cudaStream_t stream) {
     // a row is units of 32 lanes x 16 elements; a warp takes 1, 2 or 4 of them, so that
     // 8 warps are enough and as few of them as may be idle (K = 7168: 7 warps x 2)
     const int units = static_cast<int>((p.K / 16u + 31u) / 32u);
+    // Per-token calls of many rows take half the warps with twice the elements: the row's
+    // two reductions weigh more there ([8192, 4096] 32.8 -> 27.8 us); with groups, and
+    // for few rows, more warps are as fast or faster ([8192, 4096] 40.3 against 40.9).
+    if (PER_TOKEN && units > 1 && units <= 16 && p.M >= kManyRows)
+        return launch_norm_variant<In, KIND, 2, PER_TOKEN>(p, (units + 1) / 2, stream);
     if (units <= 8) return launch_norm_variant<In, KIND, 1, PER_TOKEN>(p, units, stream);
     if (units <= 16)
         return launch_norm_variant<In, KIND, 2, PER_TOKEN>(p, (units + 1) / 2, stream);
