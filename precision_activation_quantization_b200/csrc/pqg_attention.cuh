@@ -30,7 +30,8 @@ struct AttentionParams {
     const int32_t *seq_lens;
     uint64_t q_stride;         // elements between tokens
     uint64_t table_stride;
-    float scale_log2;          // sm_scale * log2(e)
+    float scale_log2;          // |sm_scale| * log2(e)
+    float sign;                // of sm_scale
     uint32_t max_pages;
     uint32_t B;
     uint32_t q_len;
@@ -41,7 +42,7 @@ struct AttentionParams {
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -1e30f;   // the running maximum before any key
+constexpr float kNoMax = -1e30f;   // a row's reference before any key
 
 // Keys of sequence b that the cache can hold.
 __device__ __forceinline__ uint32_t sequence_length(const AttentionParams &p, uint32_t b) {
@@ -170,6 +171,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// The low (high) half of a pair, twice.
+__device__ __forceinline__ uint32_t both_halves(uint32_t v, bool high) {
+    const __half2 h = *reinterpret_cast<const __half2 *>(&v);
+    const __half2 r = high ? __high2half2(h) : __low2half2(h);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
 
 // N consecutive words of read-only global memory, N in {1, 2, 4, 8}.
 template <int N>
@@ -184,6 +191,20 @@ __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[N]) {
             asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
                          : "l"(p + 4 * i));
+    }
+}
+
+// N consecutive words, N a multiple of 2, that another kernel of the call has written.
+template <int N>
+__device__ __forceinline__ void load_written(const float *p, float (&v)[N]) {
+    if constexpr (N == 2) {
+        asm volatile("ld.global.cg.v2.f32 {%0,%1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            asm volatile("ld.global.cg.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3])
+                         : "l"(p + i));
     }
 }
 
@@ -255,8 +276,10 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // so warps never wait on one another before the join.  A tile's rows are laid out
 // so that the lanes of one load meet 32 different banks (row_at below).
 //
-// The running maximum moves only when a score exceeds it by 2^8 (binary16 has
-// the room), so most tiles neither reduce it across lanes nor rescale.
+// The reference m of a row's weights 2^(score - m) lies 7 below a maximum: weights
+// near it are 2^7, so that small ones keep their bits in binary16, and m moves only
+// when a score exceeds it by 15, so that most tiles neither reduce a maximum across
+// lanes nor rescale.
 
 // A row of the first product's M, i.e. a lane's token of the tile:
 //   m-tile mt, rows gid and gid + 8  ->  tokens 4 gid + 2 mt and 4 gid + 2 mt + 1.
@@ -439,7 +462,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
         // 2^(14 - exponent), at most 2^126 (so that its reciprocal is normal)
         const int e = static_cast<int>(__float_as_uint(top) >> 23);
         const int up = min(max(268 - e, 14), 253);
-        const float grow = __uint_as_float(static_cast<uint32_t>(up) << 23);
+        const float grow = p.sign * __uint_as_float(static_cast<uint32_t>(up) << 23);
         if (tig == 0u)
             smem.shrinks[warp * kTileRows + gid] =
                 __uint_as_float(static_cast<uint32_t>(254 - up) << 23);
@@ -535,7 +558,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                 decode_e4m3x4(ksc[g], h);
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    ks[g][x] = __byte_perm(h[x >> 1], 0, x & 1 ? 0x3232 : 0x1010);
+                    ks[g][x] = both_halves(h[x >> 1], x & 1);
             }
         } else {
             uint32_t top = kref * 0x00010001u;
@@ -558,7 +581,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                 const uint32_t odd = relative_power2((ksc[g] >> 8) & 0x00FF00FFu, ref2);
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    ks[g][x] = __byte_perm(x & 1 ? odd : even, 0, x & 2 ? 0x3232 : 0x1010);
+                    ks[g][x] = both_halves(x & 1 ? odd : even, x & 2);
             }
         }
         uint32_t kraw[4][KW];
@@ -612,31 +635,32 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
         uint32_t weights[NT][4];               // B operand: [2 * k-step + half]
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float s[4][2];                     // [token][column]
+            // c[token / 2][.][2 (token & 1) + column]; the factors are not negative, so the
+            // largest product gives the largest score
+            bool seen[4][2];
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) s[x][k] = c[x >> 1][nt][2 * (x & 1) + k] * scale[nt][k];
-            if constexpr (EDGE) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        if ((gid < 4u ? now[0] : now[1]) < 0 ||
-                            static_cast<int>(k_first + x) >= limit[nt][k] - static_cast<int>(j))
-                            s[x][k] = -INFINITY;
-            }
+                for (int k = 0; k < 2; ++k) {
+                    seen[x][k] = true;
+                    if constexpr (EDGE) {
+                        seen[x][k] = (gid < 4u ? now[0] : now[1]) >= 0 &&
+                                     static_cast<int>(k_first + x) < limit[nt][k] - static_cast<int>(j);
+                        if (!seen[x][k]) c[x >> 1][nt][2 * (x & 1) + k] = -INFINITY;
+                    }
+                }
             float top[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-                top[k] = fmaxf(fmaxf(s[0][k], s[1][k]), fmaxf(s[2][k], s[3][k]));
-            if (__any_sync(0xFFFFFFFFu, top[0] > m[nt][0] + 8.0f || top[1] > m[nt][1] + 8.0f)) {
+                top[k] = scale[nt][k] * fmaxf(fmaxf(c[0][nt][k], c[0][nt][2 + k]),
+                                              fmaxf(c[1][nt][k], c[1][nt][2 + k]));
+            if (__any_sync(0xFFFFFFFFu, top[0] > m[nt][0] + 15.0f || top[1] > m[nt][1] + 15.0f)) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1)
                         top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], o));
-                    const float next = fmaxf(m[nt][k], top[k]);
+                    const float next = fmaxf(m[nt][k], top[k] - 7.0f);
                     const float fade = ex2_approx(m[nt][k] - next);
                     m[nt][k] = next;
                     l[nt][k] *= fade;
@@ -649,11 +673,14 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
             }
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float w0 = ex2_approx(s[x][0] - (m[nt][0] - 7.0f));
-                const float w1 = ex2_approx(s[x][1] - (m[nt][1] - 7.0f));
-                l[nt][0] += w0;
-                l[nt][1] += w1;
-                weights[nt][x] = transpose8x8(narrow2<__half>(w0, w1));
+                float w[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    w[k] = ex2_approx(fmaf(c[x >> 1][nt][2 * (x & 1) + k], scale[nt][k], -m[nt][k]));
+                    if (EDGE && !seen[x][k]) w[k] = 0.0f;
+                    l[nt][k] += w[k];
+                }
+                weights[nt][x] = transpose8x8(narrow2<__half>(w[0], w[1]));
             }
         }
 
@@ -777,7 +804,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
             *reinterpret_cast<uint32_t *>(p.out + (slot * D + d) * 2u) =
                 narrow2<In>(x * norm, y * norm);
             if (d == 0u && p.lse != nullptr)
-                p.lse[slot] = sum > 0.0f ? (top - 7.0f + log2f(sum)) * kLn2 : -INFINITY;
+                p.lse[slot] = sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
         } else {
             const uint64_t at = static_cast<uint64_t>(place) * R + r;
             *reinterpret_cast<float2 *>(p.part + at * D + d) = make_float2(x, y);
@@ -830,76 +857,93 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks(D, N
 constexpr int kJoinWarps = 4;
 constexpr int kJoinThreads = kJoinWarps * 32;
 
-// Joins the parts of one query row's unit: a block per row, whose warps take every
-// fourth part each.  The order of the sums is fixed.
-template <typename In, int G, int D, int NT>
+// Joins the parts of query rows' units.  A block takes ROWS rows: one, whose parts its
+// warps share (few rows, of many parts), or four, a warp each (many rows, of which
+// most have no more than a few parts).  The order of a row's sums is fixed.
+template <typename In, int G, int D, int NT, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads)
     attention_join_kernel(const __grid_constant__ AttentionParams p) {
+    static_assert(ROWS == 1 || ROWS == kJoinWarps, "a row per block or per warp");
     constexpr int E = D / 32;                  // elements a lane sums
     constexpr uint32_t R = NT * kTileRows;
-    __shared__ float sums[kJoinWarps][D];
+    constexpr uint32_t kSharing = kJoinWarps / ROWS;          // warps of a row
+    __shared__ float sums[ROWS == 1 ? kJoinWarps : 1][D];
     wait_for_producer();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
-    const uint32_t r = blockIdx.x % p.rows, bh = blockIdx.x / p.rows;
-    const uint32_t head = bh % p.c.heads, b = bh / p.c.heads;
-    const uint2 join = p.joins[static_cast<uint64_t>(bh) * p.row_tiles + r / R];
-    const uint32_t used = join.y;
+    const uint32_t turn = ROWS == 1 ? warp : 0u;              // of the warps of a row
+    const uint32_t unit_row = blockIdx.x * ROWS + (ROWS == 1 ? 0u : warp);   // < 2^31 + 4
+    const uint32_t bh = unit_row / p.rows, r = unit_row - bh * p.rows;
+    const uint32_t b = bh / p.c.heads, head = bh - b * p.c.heads;
+    uint2 join = make_uint2(0u, 0u);
+    if (b < p.B) join = __ldcg(p.joins + static_cast<uint64_t>(bh) * p.row_tiles + r / R);
+    const uint32_t used = join.y;              // the same in all warps of a row
     if (used > 1u) {
         // part 0, then the first place of each later share
         auto part_at = [&](uint32_t c) {
             return static_cast<uint64_t>(c == 0u ? join.x : (join.x / 2u + c) * 2u) * R + r % R;
         };
-        float m = kNoMax, l = 0.0f, acc[E];
+        float m, l = 0.0f, acc[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = 0.0f;
-        for (uint32_t c = lane; c < used; c += 32u)
-            m = fmaxf(m, p.stat[part_at(c)].x);
+        float2 st = make_float2(kNoMax, 0.0f);
+        if (lane < used) st = __ldcg(p.stat + part_at(lane));
+        m = st.x;
+        for (uint32_t c = lane + 32u; c < used; c += 32u)
+            m = fmaxf(m, __ldcg(p.stat + part_at(c)).x);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        // 32 parts at a time: a lane holds one part's factor, and every warp
-        // adds the values of 8 of them
+        // 32 parts at a time: a lane holds one part's factor, and every warp of the
+        // row adds the values of its turns
         for (uint32_t c0 = 0; c0 < used; c0 += 32u) {
-            float f = 0.0f;
-            if (c0 + lane < used) {
-                const float2 st = p.stat[part_at(c0 + lane)];
-                f = ex2_approx(st.x - m);
-                l = fmaf(st.y, f, l);
+            if (c0 > 0u) {
+                st = make_float2(kNoMax, 0.0f);
+                if (c0 + lane < used) st = __ldcg(p.stat + part_at(c0 + lane));
             }
+            const float f = ex2_approx(st.x - m);
+            l = fmaf(st.y, f, l);
+            // four loads in flight; past the last part its values with a factor of 0
+            for (uint32_t i = 0; i < 32u && c0 + i < used; i += 4u * kSharing) {
+                float v[4][E];
 #pragma unroll
-            for (uint32_t i = 0; i < 32u / kJoinWarps; ++i) {
-                const uint32_t c = c0 + i * kJoinWarps + warp;
-                const float fc = __shfl_sync(0xFFFFFFFFu, f, i * kJoinWarps + warp);
-                if (c < used) {                // warp-uniform
-                    uint32_t v[E];
-                    load_words(reinterpret_cast<const uint8_t *>(
-                                   p.part + part_at(c) * D + lane * E),
-                               v);
+                for (uint32_t k = 0; k < 4; ++k)
+                    load_written(p.part + part_at(min(c0 + i + k * kSharing + turn, used - 1u)) * D +
+                                     lane * E, v[k]);
 #pragma unroll
-                    for (int k = 0; k < E; ++k) acc[k] = fmaf(__uint_as_float(v[k]), fc, acc[k]);
+                for (uint32_t k = 0; k < 4; ++k) {
+                    const float fc = __shfl_sync(0xFFFFFFFFu, f, (i + k * kSharing + turn) & 31u);
+#pragma unroll
+                    for (int x = 0; x < E; ++x) acc[x] = fmaf(v[k][x], fc, acc[x]);
                 }
             }
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-#pragma unroll
-        for (int k = 0; k < E; ++k) sums[warp][lane * E + k] = acc[k];
-        __syncthreads();
         const float inv_v = G == 16 ? __frcp_rn(__ldg(p.c.gscale + 1)) : 1.0f;
         const float norm = l > 0.0f ? inv_v / l : 0.0f;
         const uint32_t t = r / p.group, qh = head * p.group + (r - t * p.group);
         const uint64_t row = (static_cast<uint64_t>(b) * p.q_len + t) * p.c.heads * p.group + qh;
-        for (uint32_t d = 2u * threadIdx.x; d < D; d += 2u * kJoinThreads) {
-            float x = 0.0f, y = 0.0f;
+        if constexpr (ROWS == 1) {
 #pragma unroll
-            for (int w = 0; w < kJoinWarps; ++w) {
-                x += sums[w][d];
-                y += sums[w][d + 1];
+            for (int k = 0; k < E; ++k) sums[warp][lane * E + k] = acc[k];
+            __syncthreads();
+            for (uint32_t d = 2u * threadIdx.x; d < D; d += 2u * kJoinThreads) {
+                float x = 0.0f, y = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kJoinWarps; ++w) {
+                    x += sums[w][d];
+                    y += sums[w][d + 1];
+                }
+                *reinterpret_cast<uint32_t *>(p.out + (row * D + d) * 2u) =
+                    narrow2<In>(x * norm, y * norm);
             }
-            *reinterpret_cast<uint32_t *>(p.out + (row * D + d) * 2u) =
-                narrow2<In>(x * norm, y * norm);
+        } else {
+#pragma unroll
+            for (int k = 0; k < E; k += 2)
+                *reinterpret_cast<uint32_t *>(p.out + (row * D + lane * E + k) * 2u) =
+                    narrow2<In>(acc[k] * norm, acc[k + 1] * norm);
         }
-        if (threadIdx.x == 0u && p.lse != nullptr)
-            p.lse[row] = l > 0.0f ? (m - 7.0f + log2f(l)) * kLn2 : -INFINITY;
+        if (lane == 0u && turn == 0u && p.lse != nullptr)
+            p.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
     release_dependents();
 }
