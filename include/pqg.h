@@ -394,7 +394,9 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
  * out      device [B * q_len][q_heads][head_dim] of in_dtype, dense, 16-byte
  *          aligned.
  * lse      device fp32 [B * q_len][q_heads], or NULL.
- * B, q_len, q_heads   B <= 2^20, q_len 1 ..= 1024, q_heads <= 16384.
+ * B, q_len, q_heads   B <= 2^20, q_len 1 ..= 1024, q_heads <= 16384, and B *
+ *          kv_heads * ceil(q_len * q_heads / kv_heads / 8) * max_pages *
+ *          page_size / 128 below 2^32 (else PQG_ERR_INVALID_ARG).
  * max_len  a hint for splitting the keys among thread blocks: the longest
  *          sequence; <= 0 means max_pages * page_size.  Sequences longer than
  *          the hint are computed in full.

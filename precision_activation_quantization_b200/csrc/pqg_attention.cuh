@@ -57,17 +57,23 @@ __device__ __forceinline__ uint32_t pieces_of(uint32_t n) {
 }
 
 // A block's share [at, end) of the pieces, and the sequence that holds piece
-// `at`, whose own pieces begin at `first`.  With P pieces in all, s = min(blocks,
-// P) shares have at least one each, and share i begins at floor(i P / s).
+// `at`, whose own pieces begin at `first`.  P pieces (the host keeps P below 2^32)
+// are dealt to s = min(blocks, P) shares: P / s each, and one more to the first P % s.
 struct Share {
-    uint64_t at, end, total, first;
-    uint32_t b, shares;
-    __device__ __forceinline__ void deal(uint64_t pieces, uint32_t blocks) {
-        total = pieces;
-        shares = static_cast<uint32_t>(min(static_cast<uint64_t>(blocks), pieces));
-        const uint64_t i = min(blockIdx.x, shares);
-        at = i * pieces / shares;
-        end = min(i + 1u, static_cast<uint64_t>(shares)) * pieces / shares;
+    uint32_t at, end, first, b;
+    uint32_t size, longer;     // pieces of a share, and how many shares have one more
+    __device__ __forceinline__ void deal(uint32_t pieces, uint32_t blocks) {
+        const uint32_t shares = min(blocks, pieces);
+        size = pieces / shares;
+        longer = pieces - size * shares;
+        const uint32_t i = min(blockIdx.x, shares);
+        at = i * size + min(i, longer);
+        end = i < shares ? at + size + (i < longer ? 1u : 0u) : at;
+    }
+    // The share that holds piece x.
+    __device__ __forceinline__ uint32_t of(uint32_t x) const {
+        const uint32_t in_longer = longer * (size + 1u);
+        return x < in_longer ? x / (size + 1u) : longer + (x - in_longer) / size;
     }
 };
 // Every thread of the block calls it.  Each sums the pieces of neighbouring
@@ -79,40 +85,37 @@ __device__ __forceinline__ Share find_share(const AttentionParams &p, uint32_t u
     s.b = 0;
     s.first = 0;
     if (p.B == 1u) {
-        s.deal(static_cast<uint64_t>(pieces_of(sequence_length(p, 0))) * units_per_sequence,
-               p.shares);
+        s.deal(pieces_of(sequence_length(p, 0)) * units_per_sequence, p.shares);
         return s;
     }
-    __shared__ uint64_t sums[THREADS / 32], found_first;
-    __shared__ uint32_t found_b;
+    __shared__ uint32_t sums[THREADS / 32], found_b, found_first;
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
     const uint32_t per = (p.B + THREADS - 1u) / THREADS;
     const uint32_t lo = min(threadIdx.x * per, p.B), hi = min(lo + per, p.B);
-    uint64_t own = 0;
+    uint32_t own = 0;
     for (uint32_t b = lo; b < hi; ++b) own += pieces_of(sequence_length(p, b));
-    uint64_t incl = own;
+    uint32_t incl = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
         if (lane >= static_cast<uint32_t>(o)) incl += v;
     }
     if (lane == 31u) sums[warp] = incl;
     __syncthreads();
-    uint64_t before = 0, all = 0;
+    uint32_t before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
         if (w < static_cast<int>(warp)) before += sums[w];
         all += sums[w];
     }
     s.deal(all * units_per_sequence, p.shares);
-    uint64_t first = (before + incl - own) * units_per_sequence;
-    if (own > 0 && first <= s.at && s.at < first + own * units_per_sequence) {
+    uint32_t first = (before + incl - own) * units_per_sequence;
+    if (first <= s.at && s.at - first < own * units_per_sequence) {
         uint32_t b = lo;
-        for (;; ++b) {                         // ends: `at` lies before the pieces' end
-            const uint64_t next =
-                first + static_cast<uint64_t>(pieces_of(sequence_length(p, b))) * units_per_sequence;
-            if (s.at < next || b + 1u >= hi) break;
-            first = next;
+        for (; b + 1u < hi; ++b) {
+            const uint32_t n = pieces_of(sequence_length(p, b)) * units_per_sequence;
+            if (s.at - first < n) break;
+            first += n;
         }
         found_b = b;
         found_first = first;
@@ -821,14 +824,12 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks(D, N
     wait_for_producer();
     const uint32_t units = p.c.heads * p.row_tiles;          // of a sequence
     Share share = find_share<Shape::kThreads>(p, units);
-    for (const uint64_t first = share.at; share.at < share.end;) {
+    for (const uint32_t first = share.at; share.at < share.end;) {
         // the unit that holds piece `at`, and its pieces in the share
         const uint32_t n = sequence_length(p, share.b), pieces = pieces_of(n);
-        const uint64_t within = share.at - share.first;
-        const uint32_t unit = static_cast<uint32_t>(within / pieces);
-        const uint32_t piece = static_cast<uint32_t>(within - static_cast<uint64_t>(unit) * pieces);
-        const uint32_t taken =
-            static_cast<uint32_t>(min(static_cast<uint64_t>(pieces - piece), share.end - share.at));
+        const uint32_t within = share.at - share.first;
+        const uint32_t unit = within / pieces, piece = within - unit * pieces;
+        const uint32_t taken = min(pieces - piece, share.end - share.at);
         // a share's first unit may have begun in another share, its last may end in one
         const uint32_t place = 2u * blockIdx.x + (share.at == first ? 0u : 1u);
         const uint32_t head = unit / p.row_tiles;
@@ -838,11 +839,8 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks(D, N
         // the block that holds a unit's first piece says where its parts are: its own
         // place, then one in every share up to the last that begins before the unit's end
         if (piece == 0u && threadIdx.x == 0u && p.joins != nullptr) {
-            const uint64_t end = share.at + pieces;
-            const uint32_t last =
-                static_cast<uint32_t>((end * share.shares - 1u) / share.total);
-            p.joins[static_cast<uint64_t>(share.b) * units + unit] =
-                make_uint2(place, taken == pieces ? 0u : last - blockIdx.x + 1u);
+            p.joins[static_cast<uint64_t>(share.b) * units + unit] = make_uint2(
+                place, taken == pieces ? 0u : share.of(share.at + pieces - 1u) - blockIdx.x + 1u);
         }
         share.at += taken;
         if (piece + taken == pieces && unit + 1u == units) {
