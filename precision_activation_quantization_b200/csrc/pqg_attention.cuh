@@ -319,15 +319,13 @@ struct AttentionShape {
     };
 };
 
-// Resident blocks per SM, which the registers are held to and a wave counts on.
-#ifndef PQG_ATT_OCC
-#define PQG_ATT_OCC 4
-#endif
-#ifndef PQG_ATT_OCC2
-#define PQG_ATT_OCC2 3
-#endif
+// Resident blocks per SM, which the registers are held to and a wave counts on: at 4
+// blocks the kernels take 119 to 128 registers; 5 blocks spill or lose more to the
+// schedule than the warps bring (64 sequences up to 8192 keys, 84.8 against 90.6 us),
+// 3 are slower too (87.3).  16 rows of a head of 128 need 3 (32 sequences with 16 query
+// heads per key head: 86.3 -> 79.4 us against 2).
 __host__ __device__ constexpr int attention_blocks(int D, int NT) {
-    return D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? PQG_ATT_OCC : PQG_ATT_OCC2) : 4;
+    return D == 128 && NT == 2 ? 3 : 4;
 }
 
 // Query rows [tile * R, + R) of (sequence b, key/value head) over keys [k_begin, k_end)
