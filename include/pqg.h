@@ -342,13 +342,14 @@ typedef struct pqg_kv_cache {
  *
  * k, v     device [T][kv_heads][head_dim] of in_dtype, 32-byte aligned; the
  *          rows of one token are dense, tokens are k_stride / v_stride
- *          elements apart (a multiple of 16, at least kv_heads * head_dim), so
+ *          elements apart (a multiple of 16, kv_heads * head_dim ..= 2^30), so
  *          both may be slices of one projection's output.
  * slots    device int32[T].  A token whose slot is negative or not below
  *          num_pages * page_size is skipped (padding).  Slots of one call are
  *          distinct; where two tokens name one slot, its contents are
  *          unspecified.
- * Slots that no token names keep their bytes.
+ * Slots that no token names keep their bytes.  Infinities and NaN are outside
+ * the contract (the codes are finite whatever the input).
  */
 PQG_API int pqg_kv_write(const pqg_kv_cache *cache, const void *k, const void *v,
               const int32_t *slots, int64_t T, int64_t k_stride, int64_t v_stride,
@@ -361,7 +362,8 @@ PQG_API int pqg_kv_write(const pqg_kv_cache *cache, const void *k, const void *v
  *   NVFP4: (code * sf) * (1 / g), in fp32, rounded once to out_dtype
  *
  * page_table  device int32[B][table_stride], of which max_pages columns are
- *          used: token j of sequence b lies in page page_table[b][j / page_size].
+ *          used (at most 2^30): token j of sequence b lies in page
+ *          page_table[b][j / page_size].  Sequences may share pages.
  *          A token whose page is not in [0, num_pages) reads as zeros.
  * indptr   device int32[B + 1], not decreasing: sequence b has
  *          indptr[b + 1] - indptr[b] tokens.  Rows of no sequence, and rows of
@@ -386,8 +388,8 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
  *
  * q        device [B * q_len][q_heads][head_dim] of in_dtype (tokens of a
  *          sequence together, oldest first), 16-byte aligned; tokens are
- *          q_stride elements apart (a multiple of 8, at least q_heads *
- *          head_dim), heads dense.  q_heads is a multiple of kv_heads; head h
+ *          q_stride elements apart (a multiple of 8, q_heads * head_dim ..=
+ *          2^30), heads dense.  q_heads is a multiple of kv_heads; head h
  *          reads key/value head h / (q_heads / kv_heads).
  * page_table, table_stride, max_pages   as for pqg_kv_read.
  * seq_lens device int32[B].

@@ -22,7 +22,7 @@ int make_plan(const CacheView &c, int64_t max_pages, int64_t B, int64_t q_len, i
               int64_t max_len, Plan *plan) {
     if (B < 0 || B > kMaxSequences || q_len < 1 || q_len > kMaxQueryTokens || q_heads < 1 ||
         q_heads % c.heads != 0 || q_heads > kMaxQueryHeads || max_pages < 1 ||
-        max_pages >= (int64_t{1} << 31))
+        max_pages > kMaxStride)
         return PQG_ERR_INVALID_ARG;
     plan->rows = q_len * (q_heads / c.heads);
     // 16 rows to a block where there are more than 8 (not for a head of 256: registers)

@@ -8,7 +8,7 @@
 namespace pqg {
 
 constexpr int64_t kMaxKvHeads = 1024;
-constexpr int64_t kMaxStride = int64_t{1} << 32;      // elements between tokens
+constexpr int64_t kMaxStride = int64_t{1} << 30;      // elements between tokens or table rows
 constexpr int64_t kMaxSequences = int64_t{1} << 20;
 constexpr int64_t kMaxQueryTokens = 1024;             // q_len
 constexpr int64_t kMaxQueryHeads = 16384;
@@ -21,8 +21,7 @@ bool overlaps_cache(const pqg_kv_cache *cache, const void *p, int64_t bytes);
 
 // A page table's shape: B rows of max_pages entries, table_stride apart.
 inline int check_table(int64_t B, int64_t table_stride, int64_t max_pages) {
-    if (B < 0 || B > kMaxSequences || max_pages < 1 || max_pages >= (int64_t{1} << 31) ||
-        table_stride < max_pages || table_stride > kMaxStride)
+    if (B < 0 || B > kMaxSequences || max_pages < 1 || table_stride < max_pages || table_stride > kMaxStride)
         return PQG_ERR_INVALID_ARG;
     return PQG_OK;
 }

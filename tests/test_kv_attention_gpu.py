@@ -195,6 +195,30 @@ def test_bad_pages_are_not_seen():
     assert (out[2] == 0).all()
 
 
+def test_sequences_may_share_pages():
+    """A common prefix held once, and one sequence listed twice."""
+    lens, P = [100, 70], 16
+    c, table = build(lens, P, 2, 64, "nvfp4")
+    table[1, :4] = table[0, :4]
+    table = torch.cat((table, table[:1]))
+    lens = [100, 70, 100]
+    q = torch.randn(3, 4, 64, device="cuda", dtype=torch.bfloat16)
+    q[2] = q[0]
+    out, lse = pqg.kv_attention(q, c, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), return_lse=True)
+    compare(out, lse, reference(q, c, table, lens, 1, 64 ** -0.5), "bf16", lens)
+    indptr = torch.tensor([0, 100, 170, 270], dtype=torch.int32, device="cuda")
+    k, v = pqg.kv_read(c, table, indptr, 270)
+    assert torch.equal(k[:64], k[100:164]) and torch.equal(v[:100], v[170:])
+
+
+def test_many_sequences():
+    """More sequences than a block has threads, and more rows than one wave takes."""
+    r = np.random.default_rng(5)
+    lens = [int(x) for x in r.integers(0, 200, 300)]
+    check(lens, 1, 8, 2, 64, 16, "mxfp4", "bf16", seed=11)
+    check([5000] + lens, 1, 4, 1, 128, 16, "nvfp4", "fp16", seed=12)
+
+
 def test_lengths_outside_the_table_are_clamped():
     c, table = build([48, 48], 16, 1, 64, "nvfp4", table_pad=0)
     q = torch.randn(2, 2, 64, device="cuda", dtype=torch.float16)

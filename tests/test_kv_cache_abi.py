@@ -140,7 +140,9 @@ LONG = dict(max_pages=4096, table_stride=4096)      # 262144 keys: split, needs 
     (dict(q_len=1025), INV), (dict(q_heads=7), INV), (dict(q_heads=0), INV),
     (dict(q_heads=16386), INV), (dict(max_pages=0), INV), (dict(table_stride=1), INV),
     (dict(sm_scale=float("nan")), INV), (dict(sm_scale=float("inf")), INV),
-    (dict(q_stride=1016), INV), (dict(q_stride=1 << 33), INV), (dict(q_stride=1028), ALN),
+    (dict(q_stride=1016), INV), (dict(q_stride=(1 << 30) + 8), INV), (dict(q_stride=1028), ALN),
+    (dict(max_pages=1 << 31, table_stride=1 << 31), INV),
+    (dict(B=1 << 20, max_pages=1 << 24, table_stride=1 << 24), INV),      # 2^44 pieces of keys
     (dict(q_ptr=0), INV), (dict(page_table_ptr=0), INV), (dict(seq_lens_ptr=0), INV),
     (dict(out_ptr=0), INV), (dict(q_ptr=at(4) + 8), ALN), (dict(out_ptr=at(7) + 8), ALN),
     (dict(lse_ptr=at(8) + 2), ALN), (dict(page_table_ptr=at(5) + 2), ALN),

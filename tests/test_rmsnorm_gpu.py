@@ -118,6 +118,16 @@ def test_x_may_be_the_output_of_the_sum():
     assert got[2] is x
 
 
+def test_leading_dimensions_are_rows():
+    x, r = (dev(rows(24, 512, s, "bf16"), "bf16") for s in (1, 2))
+    w = torch.ones(512, dtype=x.dtype, device="cuda")
+    want = pqg.rmsnorm_quant(x, w, r)
+    got = pqg.rmsnorm_quant(x.view(2, 12, 512), w, r.view(2, 12, 512))
+    assert got[0].shape == (24, 512) and got[2].shape == (2, 12, 512)
+    for a, b in zip(want, got):
+        assert torch.equal(a.view(torch.uint8), b.reshape(a.shape).view(torch.uint8))
+
+
 @pytest.mark.parametrize("eps", [0.0, 1e-12, 1e-5, 3.0])
 def test_eps(eps):
     # eps = 0 with an all-zero row is outside the contract: M = 2 has none
