@@ -155,13 +155,18 @@ def code_only(text: str) -> str:
     return "\n".join(l.rstrip() for l in text.splitlines() if l.strip())
 
 
+# the sources of the kernels this file times (csrc/ holds the library's others too)
+QUANT_SOURCES = ("pqg_api.cu", "pqg_host.cuh", "pqg_kernel.cuh", "pqg_launch.cuh",
+                 "pqg_launch_bf16.cu", "pqg_launch_fp16.cu", "pqg_row_kernel.cuh")
+
+
 def source_digest(kernel: str = "strip") -> str:
     """sha256 over the code of the CUDA sources a kernel is built from (the
     strip kernel does not include the per-token row kernel's file), to tell
     whether stored ncu counters still apply."""
     csrc = os.path.join(ROOT, "precision_activation_quantization_b200", "csrc")
     h = hashlib.sha256()
-    for f in sorted(os.listdir(csrc)):
+    for f in QUANT_SOURCES:
         if kernel == "strip" and f == "pqg_row_kernel.cuh":
             continue
         with open(os.path.join(csrc, f), encoding="utf-8") as fh:
