@@ -406,8 +406,12 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
  *          pqg_kv_attention_workspace(...) bytes for the same arguments,
  *          16-byte aligned (NULL when that is 0).  Its contents are dead
  *          after the call; calls that may run at the same time need one each.
- * Keys and values are used exactly as stored; queries exactly; the softmax
- * weights are rounded to 11 bits for the product with V, sums are in fp32.
+ * Keys, values and queries enter the products exactly, except that (MXFP4) a
+ * group of keys or values whose scale is 2^-27 or less of the largest one the
+ * same warp has met before it counts as zero.  The softmax weights are rounded
+ * to 11 bits for the product with V; sums are in fp32.  Results do not depend
+ * on anything but the arguments (no atomics), max_len and the number of the
+ * device's SMs included.
  */
 PQG_API int pqg_kv_attention(const pqg_kv_cache *cache, const void *q, int64_t q_stride,
               const int32_t *page_table, int64_t table_stride, int64_t max_pages,

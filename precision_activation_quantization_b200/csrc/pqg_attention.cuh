@@ -256,12 +256,11 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // s_jg) / sum_j p_j.  Both products run on the tensor cores in binary16 with
 // fp32 sums, and their operands are exact: a code has 2 significant bits and an
 // E4M3 scale 4, so their product is a binary16 number.  A UE8M0 scale has a
-// wider range than binary16, so it is taken relative to the largest scale of the
-// tile's keys, or, for the values, the largest so far of the lane's elements
-// (12 binades above 1; scales 2^-26 below the largest count as zero).  A query
+// wider range than binary16, so it is taken relative to a reference, 12 binades above
+// 1: the largest scale so far of the warp's keys, or of the lane's elements of the
+// values.  A group whose scale is 2^-27 of the reference or less counts as zero.  A query
 // row is scaled by a power of two into [2^14, 2^15).  Only the weights p are
-// rounded, to binary16's 11 bits, at 2^7 times their size so that small ones keep
-// their bits.
+// rounded, to binary16's 11 bits.
 //
 // Layout.  A warp takes 32 keys at a time; tokens are M of the first product, so
 // that 8 query rows (N) cost no more tensor work than one.  The order of a sum's
@@ -283,9 +282,19 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // near it are 2^7, so that small ones keep their bits in binary16, and m moves only
 // when a score exceeds it by 15, so that most tiles neither reduce a maximum across
 // lanes nor rescale.
+//
+// Measured.  64 ragged sequences of up to 8192 keys, 32 query and 8 key heads of 128:
+// 348 MB of MXFP4 in 83 us (4.2 TB/s), 367 MB of NVFP4 in 78 us (4.7); one sequence
+// of 131072 keys, 151 MB, in 39 us.  HBM would take 53, 56 and 23.  What bounds it is
+// the mixture of one tensor instruction, four conversions and four binary16
+// multiplications that 16 keys x 16 elements need: each of the three alone takes 2.0
+// clocks of an SM, two of them 2.5 to 3.6, but all together 5.0, at any occupancy, and
+// a tile is 32 such groups, 160 of its 250 clocks.  Blocks of 12 or 20 warps an SM are
+// slower than 16, and moving the shifts to the multiplier changes nothing.
 
-// A row of the first product's M, i.e. a lane's token of the tile:
-//   m-tile mt, rows gid and gid + 8  ->  tokens 4 gid + 2 mt and 4 gid + 2 mt + 1.
+// (A lane's tokens as rows of the first product's M: m-tile mt, rows gid and gid + 8
+// are tokens 4 gid + 2 mt and 4 gid + 2 mt + 1.)
+
 // Where 16-byte part c of token r's codes lies in a tile of keys (values).
 // Lanes of one load differ in r / 4 (keys, read by gid) or r / 8 (values, read by
 // tig); those bits choose among the places of equal banks.
