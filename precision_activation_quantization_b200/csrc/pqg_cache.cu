@@ -60,6 +60,10 @@ bool overlaps_cache(const pqg_kv_cache *cache, const void *p, int64_t bytes) {
 
 }  // namespace pqg
 
+namespace {
+constexpr int64_t kManyReads = 4 * 2 * 148 * 2048;   // 16-element pieces of the output
+}
+
 extern "C" {
 
 int pqg_kv_write(const pqg_kv_cache *cache, const void *k, const void *v, const int32_t *slots,
@@ -112,7 +116,9 @@ int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table, int64_t ta
     if (ts != PQG_OK) return ts;
     const int64_t row = static_cast<int64_t>(cache->kv_heads) * cache->head_dim;
     if (M < 0 || M >= (int64_t{1} << 31)) return PQG_ERR_INVALID_ARG;
-    const int64_t rowheads = (M + kReadRows - 1) / kReadRows * cache->kv_heads;
+    // four rows a thread where that still gives the SMs two waves of threads
+    const bool many = M * row / 16 >= kManyReads;
+    const int64_t rowheads = (M + (many ? 3 : 0)) / (many ? 4 : 1) * cache->kv_heads;
     const int64_t blocks = (rowheads * (cache->head_dim / 16) + kCacheThreads - 1) / kCacheThreads;
     if (rowheads > (int64_t{1} << 31) - kCacheThreads) return PQG_ERR_INVALID_ARG;
     if (M == 0 || B == 0) return PQG_OK;
@@ -136,8 +142,12 @@ int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table, int64_t ta
     p.B = static_cast<uint32_t>(B);
     p.M = static_cast<uint32_t>(M);
     const bool nv = cache->format == PQG_KV_NVFP4, bf = out_dtype == PQG_BF16;
-    auto kernel = bf ? (nv ? kv_read_kernel<__nv_bfloat16, 16> : kv_read_kernel<__nv_bfloat16, 32>)
-                     : (nv ? kv_read_kernel<__half, 16> : kv_read_kernel<__half, 32>);
+    auto kernel = many ? (bf ? (nv ? kv_read_kernel<__nv_bfloat16, 16, 4>
+                                   : kv_read_kernel<__nv_bfloat16, 32, 4>)
+                             : (nv ? kv_read_kernel<__half, 16, 4> : kv_read_kernel<__half, 32, 4>))
+                       : (bf ? (nv ? kv_read_kernel<__nv_bfloat16, 16, 1>
+                                   : kv_read_kernel<__nv_bfloat16, 32, 1>)
+                             : (nv ? kv_read_kernel<__half, 16, 1> : kv_read_kernel<__half, 32, 1>));
     return launched(launch(kernel, blocks, kCacheThreads, 0,
                            reinterpret_cast<cudaStream_t>(stream), p), 1);
 }

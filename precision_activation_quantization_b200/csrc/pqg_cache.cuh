@@ -174,14 +174,14 @@ __device__ __forceinline__ float ue8m0_value(uint32_t e) {
     return e == 0u ? __uint_as_float(0x00400000u) : __uint_as_float(e << 23);
 }
 
-// One lane decodes 16 elements of the key rows and of the value rows of kReadRows
-// neighbouring output rows, so that finding the sequence and the page is shared
-// and eight loads of codes are in flight.  Bound by the 16-bit output: 80 MB read and
-// 283 MB written in 67 us; a plain fill of memory writes 3.9 TB/s here, at which the
-// output alone takes 72 us (part of it is still in L2 when the call ends).
-constexpr uint32_t kReadRows = 4;
-
-template <typename Out, int G>
+// One lane decodes 16 elements of the key rows and of the value rows of ROWS
+// neighbouring output rows: 4 where there are many, so that finding the sequence is
+// shared and eight loads of codes are in flight, 1 where the rows would not fill the
+// SMs otherwise (7 sequences of up to 300 tokens: 2.1 us against 4.4).  The pages of all
+// rows are asked for before any code.  Bound by the 16-bit output: 363 MB in 59.5 us
+// (6.1 TB/s, 0.93 of the copy rate); 67 us when a row's codes were asked for before the
+// next row's page.
+template <typename Out, int G, int ROWS>
 __global__ void __launch_bounds__(kCacheThreads)
     kv_read_kernel(const __grid_constant__ ReadParams p) {
     wait_for_producer();
@@ -190,52 +190,56 @@ __global__ void __launch_bounds__(kCacheThreads)
     const uint32_t col = (static_cast<uint32_t>(unit) & ((1u << lane_shift) - 1u)) * 16u;
     const uint32_t rowhead = static_cast<uint32_t>(unit >> lane_shift);   // < 2^31
     const uint32_t group = div_heads(p.c, rowhead), head = rowhead - group * p.c.heads;
-    const uint64_t row0 = static_cast<uint64_t>(group) * kReadRows;
+    const uint64_t row0 = static_cast<uint64_t>(group) * ROWS;
     if (row0 < p.M) {
         const float inv[2] = {G == 16 ? __frcp_rn(__ldg(p.c.gscale)) : 1.0f,
                               G == 16 ? __frcp_rn(__ldg(p.c.gscale + 1)) : 1.0f};
-        uint2 codes[kReadRows][2];
-        uint32_t scale[kReadRows][2];
-        bool held[kReadRows], good[kReadRows];
+        uint2 codes[ROWS][2];
+        uint32_t scale[ROWS][2], at[ROWS];     // at: token of its sequence
+        int page[ROWS];
+        bool held[ROWS];
         int b = -1, first = 0, last = INT32_MIN;    // the sequence and its rows [first, last)
 #pragma unroll
-        for (uint32_t i = 0; i < kReadRows; ++i) {
+        for (uint32_t i = 0; i < ROWS; ++i) {
             const uint64_t row = row0 + i;
-            held[i] = good[i] = false;
+            held[i] = false;
+            page[i] = -1;
+            at[i] = 0u;
             if (row < p.M) {
-                if (i == 0u || static_cast<int>(row) >= last) {
+                if (static_cast<int>(row) >= last) {
                     b = find_sequence(p.indptr, p.B, static_cast<int>(row), &first);
                     last = b >= 0 ? __ldg(p.indptr + b + 1) : static_cast<int>(row) + 1;
                 }
-                const uint32_t j = static_cast<uint32_t>(row) - static_cast<uint32_t>(first);
-                held[i] = b >= 0 && (j >> p.c.page_shift) < p.max_pages;
-                if (held[i]) {
-                    const int page = __ldg(p.table + static_cast<uint64_t>(b) * p.table_stride +
-                                           (j >> p.c.page_shift));
-                    good[i] = static_cast<uint32_t>(page) < p.c.num_pages;
-                    if (good[i]) {
-                        const uint32_t off = j & ((1u << p.c.page_shift) - 1u);
-                        const uint64_t at = code_offset(p.c, page, head, off) + col / 2u;
-                        const uint64_t sc = scale_offset<G>(p.c, page, head, col / G, off);
+                at[i] = static_cast<uint32_t>(row) - static_cast<uint32_t>(first);
+                held[i] = b >= 0 && (at[i] >> p.c.page_shift) < p.max_pages;
+                if (held[i])
+                    page[i] = __ldg(p.table + static_cast<uint64_t>(b) * p.table_stride +
+                                    (at[i] >> p.c.page_shift));
+            }
+        }
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            codes[i][n] =
-                                __ldg(reinterpret_cast<const uint2 *>(p.c.codes[n] + at));
-                            scale[i][n] = __ldg(p.c.scales[n] + sc);
-                        }
-                    }
+        for (uint32_t i = 0; i < ROWS; ++i) {
+            if (static_cast<uint32_t>(page[i]) >= p.c.num_pages) page[i] = -1;
+            if (page[i] >= 0) {
+                const uint32_t off = at[i] & ((1u << p.c.page_shift) - 1u);
+                const uint64_t code = code_offset(p.c, page[i], head, off) + col / 2u;
+                const uint64_t sc = scale_offset<G>(p.c, page[i], head, col / G, off);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    codes[i][n] = __ldg(reinterpret_cast<const uint2 *>(p.c.codes[n] + code));
+                    scale[i][n] = __ldg(p.c.scales[n] + sc);
                 }
             }
         }
 #pragma unroll
-        for (uint32_t i = 0; i < kReadRows; ++i) {
+        for (uint32_t i = 0; i < ROWS; ++i) {
             if (!held[i]) continue;
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 uint32_t w[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) w[k] = 0u;
-                if (good[i]) {
+                if (page[i] >= 0) {
                     const float s = G == 16 ? e4m3_code_value(scale[i][n] & 0x7Fu)
                                             : ue8m0_value(scale[i][n]);
                     decode8<Out, G == 16>(codes[i][n].x, s, inv[n], w);

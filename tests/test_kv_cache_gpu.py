@@ -131,6 +131,49 @@ def test_read_back_values(fmt, out_dtype, D, P, H):
     check_read([P, 3 * P + 1, 0, 2 * P - 1, 0], P, H, D, fmt, out_dtype, lead=3, seed=1, table_pad=3)
 
 
+@pytest.mark.parametrize("fmt,out_dtype", [("mxfp4", "fp16"), ("nvfp4", "bf16")])
+@pytest.mark.parametrize("D,P,H", [(64, 16, 8), (128, 32, 5), (256, 64, 3)])
+def test_read_many_rows(fmt, out_dtype, D, P, H):
+    """Calls large enough to take several rows a thread: sequences of every length
+    from 0, starting anywhere, sharing pages; a page outside the cache; a gap before
+    the first row and rows behind the last."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    pages, rows_wanted = 64, 2 * 4 * 148 * 2048 * 16 // (H * D) + 1000
+    c, _ = filled(pages, P, H, D, fmt)
+    lo, hi = (100, 135) if fmt == "mxfp4" else (0, 127)
+    for n in ("k", "v"):
+        codes, scales = getattr(c, n + "_codes"), getattr(c, n + "_scales")
+        codes.copy_(torch.randint(0, 256, codes.shape, generator=g, device="cuda", dtype=torch.uint8))
+        scales.copy_(torch.randint(lo, hi, scales.shape, generator=g, device="cuda", dtype=torch.uint8))
+    lens = np.random.default_rng(D).integers(0, 9, 1000).tolist() + [0, 1, 2, 3]
+    lens += [700] * ((rows_wanted - sum(lens)) // 700 + 1)
+    table = torch.randint(0, pages, (len(lens), 700 // P + 1), generator=g, device="cuda", dtype=torch.int32)
+    table[5, 0] = pages
+    indptr = np.concatenate(([0], np.cumsum(lens))) + 7
+    M = int(indptr[-1]) + 9
+    ip = torch.from_numpy(indptr.astype(np.int32)).cuda()
+    out = [torch.full((M, H, D), -3.0, dtype=DT[out_dtype], device="cuda") for _ in range(2)]
+    pqg.kv_read(c, table, ip, M, k_out=out[0], v_out=out[1])
+    row = torch.arange(7, M - 9, device="cuda")
+    b = torch.bucketize(row, ip[1:].long(), right=True)
+    j = row - ip.long()[b]
+    page, off = table[b, j // P].long(), j % P
+    bad = page >= pages
+    page = page.clamp(max=pages - 1)
+    e2m1 = torch.tensor(ref.E2M1, dtype=torch.float32, device="cuda")
+    for n, (codes, scales) in enumerate(((c.k_codes, c.k_scales), (c.v_codes, c.v_scales))):
+        assert (out[n][:7] == -3).all() and (out[n][M - 9:] == -3).all()
+        s = scales.transpose(-1, -2)
+        s = torch.exp2(s.float() - 127) if fmt == "mxfp4" else s.view(torch.float8_e4m3fn).float()
+        x = torch.stack((e2m1[(codes & 15).long()], e2m1[(codes >> 4).long()]), -1).flatten(-2)
+        x = x * s.repeat_interleave(ref.GROUP[fmt], -1)
+        if fmt == "nvfp4":
+            x = x * (torch.ones((), device="cuda") / torch.tensor(G_SCALE[n], device="cuda"))
+        want = x.to(DT[out_dtype])[page, :, off]
+        want[bad] = 0
+        assert torch.equal(out[n][7:M - 9].view(torch.int16), want.view(torch.int16))
+
+
 def test_read_bad_pages_are_zeros():
     check_read([40, 100, 17], 16, 2, 64, "mxfp4", "bf16", bad=True)
 
