@@ -407,9 +407,12 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
  *          16-byte aligned (NULL when that is 0).  Its contents are dead
  *          after the call; calls that may run at the same time need one each.
  * Keys, values and queries enter the products exactly, except that (MXFP4) a
- * group of keys or values whose scale is 2^-27 or less of the largest one the
- * same warp has met before it counts as zero.  The softmax weights are rounded
- * to 11 bits for the product with V; sums are in fp32.  Results do not depend
+ * group of values whose scale is 2^-27 or less of the largest one that the
+ * same elements have met counts as zero, a group of keys with scale byte 0
+ * too; keys' scales from 2^118 on may give a score that is not finite.  The
+ * softmax weights are rounded to 11 bits for the product with V; sums are in
+ * fp32.  A row whose query holds a NaN has out and lse NaN, once it sees a
+ * key; other rows are not touched by it.  Results do not depend
  * on anything but the arguments (no atomics), max_len and the number of the
  * device's SMs included.
  */

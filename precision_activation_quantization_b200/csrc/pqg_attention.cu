@@ -67,9 +67,10 @@ cudaError_t launch_rows(const AttentionParams &p, const Plan &plan, cudaStream_t
     *kernels = 2;
     const int64_t rows = static_cast<int64_t>(p.B) * p.c.heads * p.rows;
     if (rows < kManyJoins)
-        return launch(attention_join_kernel<In, G, D, NT, 1>, rows, kJoinThreads, 0, stream, p);
-    return launch(attention_join_kernel<In, G, D, NT, kJoinWarps>,
-                  (rows + kJoinWarps - 1) / kJoinWarps, kJoinThreads, 0, stream, p);
+        return launch(attention_join_kernel<In, G, D, NT, 1>, rows, join_warps(1) * 32, 0,
+                      stream, p);
+    return launch(attention_join_kernel<In, G, D, NT, 4>, (rows + 3) / 4, join_warps(4) * 32, 0,
+                  stream, p);
 }
 
 template <typename In, int G, int D>
@@ -168,7 +169,8 @@ int pqg_kv_attention(const pqg_kv_cache *cache, const void *q, int64_t q_stride,
     p.q_stride = static_cast<uint64_t>(q_stride);
     p.table_stride = static_cast<uint64_t>(table_stride);
     // a negative scale goes to the queries, so that larger products are larger scores
-    p.scale_log2 = static_cast<float>(std::fabs(static_cast<double>(sm_scale)) * 1.4426950408889634);
+    p.scale_log2 =
+        static_cast<float>(std::fabs(static_cast<double>(sm_scale)) * 1.4426950408889634);
     p.sign = sm_scale < 0.0f ? -1.0f : 1.0f;
     p.max_pages = static_cast<uint32_t>(max_pages);
     p.B = static_cast<uint32_t>(B);

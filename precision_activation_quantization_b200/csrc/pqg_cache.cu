@@ -147,7 +147,8 @@ int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table, int64_t ta
                              : (nv ? kv_read_kernel<__half, 16, 4> : kv_read_kernel<__half, 32, 4>))
                        : (bf ? (nv ? kv_read_kernel<__nv_bfloat16, 16, 1>
                                    : kv_read_kernel<__nv_bfloat16, 32, 1>)
-                             : (nv ? kv_read_kernel<__half, 16, 1> : kv_read_kernel<__half, 32, 1>));
+                             : (nv ? kv_read_kernel<__half, 16, 1>
+                                    : kv_read_kernel<__half, 32, 1>));
     return launched(launch(kernel, blocks, kCacheThreads, 0,
                            reinterpret_cast<cudaStream_t>(stream), p), 1);
 }

@@ -21,7 +21,8 @@ bool overlaps_cache(const pqg_kv_cache *cache, const void *p, int64_t bytes);
 
 // A page table's shape: B rows of max_pages entries, table_stride apart.
 inline int check_table(int64_t B, int64_t table_stride, int64_t max_pages) {
-    if (B < 0 || B > kMaxSequences || max_pages < 1 || table_stride < max_pages || table_stride > kMaxStride)
+    if (B < 0 || B > kMaxSequences || max_pages < 1 || table_stride < max_pages ||
+        table_stride > kMaxStride)
         return PQG_ERR_INVALID_ARG;
     return PQG_OK;
 }

@@ -185,6 +185,12 @@ def test_scales_far_apart():
     check([200], 1, 4, 1, 128, 16, "mxfp4", "fp16", spread=(118, 127), q_size=20000.0, sm_scale=1e-6)
 
 
+def test_scales_near_the_ends():
+    """MXFP4 keys' scales up to 2^117 (with codes and queries: sums of 2^124), and down to 2^-126."""
+    check([200], 1, 4, 1, 64, 32, "mxfp4", "bf16", spread=(238, 245), sm_scale=1.0, q_size=2.0 ** -116)
+    check([200], 1, 9, 1, 256, 16, "mxfp4", "bf16", spread=(1, 8), sm_scale=1.0, q_size=2.0 ** 112)
+
+
 def test_bad_pages_are_not_seen():
     lens, P = [100, 64, 40], 16
     c, table = build(lens, P, 2, 64, "mxfp4")
@@ -237,6 +243,22 @@ def test_masked_queries_are_not_read_into_others():
     q2[0], q2[1] = torch.inf, torch.nan           # tokens 0 and 1 of the first sequence see no key
     got = pqg.kv_attention(q2, c, table, n)
     assert (got[:2] == 0).all() and torch.equal(got[2:], want[2:])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_a_nan_query_spoils_its_own_row(fmt):
+    """One head's row, in a whole unit and in one that is split; other rows keep their bits."""
+    lens = [40, 30000]
+    c, table = build(lens, 32, 2, 128, fmt)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 6, 128, device="cuda", dtype=torch.bfloat16)
+    want, wl = pqg.kv_attention(q, c, table, n, return_lse=True)
+    bad = torch.zeros(2, 6, dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[1, 4] = True
+    q[0, 1], q[1, 4, 77] = torch.nan, torch.nan
+    got, lse = pqg.kv_attention(q, c, table, n, return_lse=True)
+    assert got[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(got[~bad], want[~bad]) and torch.equal(lse[~bad], wl[~bad])
 
 
 def test_deterministic_other_stream_graph_and_two_at_once():
