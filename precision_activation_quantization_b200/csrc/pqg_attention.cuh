@@ -295,7 +295,7 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // lanes nor rescale.
 //
 // Measured.  64 ragged sequences of up to 8192 keys, 32 query and 8 key heads of 128:
-// 348 MB of MXFP4 in 80 us (4.3 TB/s), 367 MB of NVFP4 in 76 us (4.9); one sequence
+// 348 MB of MXFP4 in 80 us (4.3 TB/s), 367 MB of NVFP4 in 75 us (4.9); one sequence
 // of 131072 keys, 151 MB, in 38 us.  HBM would take 53, 56 and 23.  What bounds it is
 // the mixture of one tensor instruction, four conversions and four binary16
 // multiplications that 16 keys x 16 elements need (without the last for MXFP4 keys):
@@ -942,6 +942,11 @@ __global__ void __launch_bounds__(join_warps(ROWS) * 32)
     constexpr int E = D / 32;                  // elements a lane sums
     constexpr uint32_t R = NT * kTileRows;
     constexpr uint32_t kSharing = kWarps / ROWS;          // warps of a row
+    // parts a warp has in flight: 32 registers of them, within a round of 32 parts (17
+    // sequences of 4 tokens and up to 2000 keys, head 64: 10.6 -> 9.8 us of the whole call
+    // against 4)
+    constexpr uint32_t kLoads = ROWS == 1 ? 32u / kSharing : 32u / E;
+    static_assert(kLoads * kSharing <= 32u, "a factor's lane is its part's place in the round");
     __shared__ float sums[ROWS == 1 ? kWarps : 1][D];
     wait_for_producer();
     const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
@@ -957,11 +962,24 @@ __global__ void __launch_bounds__(join_warps(ROWS) * 32)
         auto part_at = [&](uint32_t c) {
             return static_cast<uint64_t>(c == 0u ? join.x : (join.x / 2u + c) * 2u) * R + r % R;
         };
+        // values of parts c + turn, c + kSharing + turn, ..; past the last one zeros.  The
+        // first are on their way before the maxima that weight them.
+        float v[kLoads][E];
+        auto fetch = [&](uint32_t c) {
+#pragma unroll
+            for (uint32_t k = 0; k < kLoads; ++k) {
+                const uint32_t mine = c + k * kSharing + turn;
+#pragma unroll
+                for (int x = 0; x < E; ++x) v[k][x] = 0.0f;
+                if (mine < used) load_written(p.part + lane * E + part_at(mine) * D, v[k]);
+            }
+        };
         float m, l = 0.0f, acc[E];
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = 0.0f;
         float2 st = make_float2(kNoMax, 0.0f);
         if (lane < used) st = __ldcg(p.stat + part_at(lane));
+        fetch(0u);
         m = st.x;
         for (uint32_t c = lane + 32u; c < used; c += 32u)
             m = fmaxf(m, __ldcg(p.stat + part_at(c)).x);
@@ -976,16 +994,10 @@ __global__ void __launch_bounds__(join_warps(ROWS) * 32)
             }
             const float f = ex2_approx(st.x - m);
             l = fmaf(st.y, f, l);
-            // four loads in flight; past the last part its values with a factor of 0
-            for (uint32_t i = 0; i < 32u && c0 + i < used; i += 4u * kSharing) {
-                float v[4][E];
+            for (uint32_t i = 0; i < 32u && c0 + i < used; i += kLoads * kSharing) {
+                if (c0 + i > 0u) fetch(c0 + i);
 #pragma unroll
-                for (uint32_t k = 0; k < 4; ++k)
-                    load_written(p.part + lane * E +
-                                     part_at(min(c0 + i + k * kSharing + turn, used - 1u)) * D,
-                                 v[k]);
-#pragma unroll
-                for (uint32_t k = 0; k < 4; ++k) {
+                for (uint32_t k = 0; k < kLoads; ++k) {
                     const float fc = __shfl_sync(0xFFFFFFFFu, f, (i + k * kSharing + turn) & 31u);
 #pragma unroll
                     for (int x = 0; x < E; ++x) acc[x] = fmaf(v[k][x], fc, acc[x]);
