@@ -296,7 +296,7 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 //
 // Measured.  64 ragged sequences of up to 8192 keys, 32 query and 8 key heads of 128:
 // 348 MB of MXFP4 in 80 us (4.3 TB/s), 367 MB of NVFP4 in 75 us (4.9); one sequence
-// of 131072 keys, 151 MB, in 38 us.  HBM would take 53, 56 and 23.  What bounds it is
+// of 131072 keys, 151 MB, in 36.5 us.  HBM would take 53, 56 and 23.  What bounds it is
 // the mixture of one tensor instruction, four conversions and four binary16
 // multiplications that 16 keys x 16 elements need (without the last for MXFP4 keys):
 // each of the three alone takes 2.0 clocks of an SM, two of them 2.5 to 3.6, but all
