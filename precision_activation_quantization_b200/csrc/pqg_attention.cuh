@@ -42,7 +42,7 @@ struct AttentionParams {
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -1e30f;   // a row's reference before any key
+constexpr float kNoMax = -3e38f;   // a row's reference before any key (finite: differences are)
 
 // Keys of sequence b that the cache can hold.
 __device__ __forceinline__ uint32_t sequence_length(const AttentionParams &p, uint32_t b) {
@@ -295,7 +295,7 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // lanes nor rescale.
 //
 // Measured.  64 ragged sequences of up to 8192 keys, 32 query and 8 key heads of 128:
-// 348 MB of MXFP4 in 80 us (4.3 TB/s), 367 MB of NVFP4 in 75 us (4.9); one sequence
+// 348 MB of MXFP4 in 79 us (4.4 TB/s), 367 MB of NVFP4 in 75 us (4.9); one sequence
 // of 131072 keys, 151 MB, in 36.5 us.  HBM would take 53, 56 and 23.  What bounds it is
 // the mixture of one tensor instruction, four conversions and four binary16
 // multiplications that 16 keys x 16 elements need (without the last for MXFP4 keys):
@@ -711,25 +711,29 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
             uint32_t weights[NT][4];               // B operand: [2 * k-step + half]
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                // c[token / 2][.][2 (token & 1) + column]; the factors are not negative, so the
-                // largest product gives the largest score
+                // Scores of token x, columns 2 tig and 2 tig + 1, rounded before anything is
+                // subtracted: the largest of them is then the reference's own number (a fused
+                // c scale - m would differ from it by up to half an ulp of a huge score).
+                float2 score[4];
                 bool seen[4][2];
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
+                for (int x = 0; x < 4; ++x) {
+                    score[x] = __fmul2_rn(make_float2(c[x >> 1][nt][2 * (x & 1)],
+                                                      c[x >> 1][nt][2 * (x & 1) + 1]),
+                                          make_float2(scale[nt][0], scale[nt][1]));
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         seen[x][k] = true;
-                        if constexpr (EDGE) {
+                        if constexpr (EDGE)
                             seen[x][k] = (gid < 4u ? now[0] : now[1]) >= 0 &&
                                          static_cast<int>(k_first + x + j) < limit[nt][k];
-                            if (!seen[x][k]) c[x >> 1][nt][2 * (x & 1) + k] = -INFINITY;
-                        }
                     }
+                    if (EDGE && !seen[x][0]) score[x].x = -INFINITY;
+                    if (EDGE && !seen[x][1]) score[x].y = -INFINITY;
+                }
                 float top[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    top[k] = scale[nt][k] * fmaxf(fmaxf(c[0][nt][k], c[0][nt][2 + k]),
-                                                  fmaxf(c[1][nt][k], c[1][nt][2 + k]));
+                top[0] = fmaxf(fmaxf(score[0].x, score[1].x), fmaxf(score[2].x, score[3].x));
+                top[1] = fmaxf(fmaxf(score[0].y, score[1].y), fmaxf(score[2].y, score[3].y));
                 if (__any_sync(0xFFFFFFFFu,
                                top[0] > m[nt][0] + 15.0f || top[1] > m[nt][1] + 15.0f)) {
 #pragma unroll
@@ -750,11 +754,10 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                 }
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    float w[2];
+                    const float2 e = __fadd2_rn(score[x], make_float2(-m[nt][0], -m[nt][1]));
+                    float w[2] = {ex2_approx(e.x), ex2_approx(e.y)};
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        w[k] = ex2_approx(
-                            fmaf(c[x >> 1][nt][2 * (x & 1) + k], scale[nt][k], -m[nt][k]));
                         if (EDGE && !seen[x][k]) w[k] = 0.0f;
                         l[nt][k] += w[k];
                     }

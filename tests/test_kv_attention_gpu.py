@@ -191,6 +191,22 @@ def test_scales_near_the_ends():
     check([200], 1, 9, 1, 256, 16, "mxfp4", "bf16", spread=(1, 8), sm_scale=1.0, q_size=2.0 ** 112)
 
 
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_huge_scores(fmt, sign):
+    """Every score beyond 1e30 in size, below or above zero: rows see their keys all the same."""
+    lens = [70, 30000]
+    c, table = build(lens, 32, 2, 128, fmt)
+    c.k_codes.bitwise_and_(0x77).bitwise_or_(0x11)                 # no key element is below 0.5 scales
+    q = torch.randn(2, 6, 128, device="cuda").abs_().add_(1.0).mul_(1e32).bfloat16()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = pqg.kv_attention(q, c, table, n, sm_scale=sign, return_lse=True)
+    want = reference(q, c, table, lens, 1, sign)
+    assert (want[1] * sign > 1e30).all()
+    compare(out, lse, want, "bf16", lens)
+    assert (out != 0).any(-1).all()
+
+
 def test_bad_pages_are_not_seen():
     lens, P = [100, 64, 40], 16
     c, table = build(lens, P, 2, 64, "mxfp4")
