@@ -293,6 +293,10 @@ PQG_API int pqg_quant_varlen(const void *in, void *out, void *scales,
  *          the device fp32 g of pqg_quant_nvfp4, else it is NULL.
  * eps      finite, >= 0.  (eps = 0 and an all-zero row: inv is infinite, y is
  *          not a number and its codes are unspecified; nothing faults.)
+ * A row with an infinite h has inv = 0: y is 0, and not a number at the
+ * infinite elements.  In a row with a NaN every y is one.  E4M3 codes of such
+ * y are NaN (codes of the other types unspecified), and a group's amax passes
+ * over them.  Other rows are not touched.
  * Returns as pqg_quant.
  */
 PQG_API int pqg_rmsnorm_quant(const void *in, const void *residual, const void *weight,

@@ -221,3 +221,22 @@ def test_refusals():
     wide = torch.zeros(1, 32768, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(pqg.PqgError):
         pqg.rmsnorm_quant(wide, wide[0])
+
+
+@pytest.mark.parametrize("scale_fmt", ["fp32", "ue8m0"])
+@pytest.mark.parametrize("K", [256, 1024, 7168])
+def test_infinities_and_nans_stay_in_their_rows(K, scale_fmt):
+    x = torch.randn(6, K, device="cuda", dtype=torch.float16)
+    w = torch.randn(K, device="cuda", dtype=torch.float16)
+    w[w == 0] = 1
+    want, ws, _ = pqg.rmsnorm_quant(x, w, scale_fmt=scale_fmt)
+    x[1, 5], x[3, K - 1], x[4, 7] = torch.inf, torch.nan, -torch.inf
+    got, gs, _ = pqg.rmsnorm_quant(x, w, scale_fmt=scale_fmt)
+    g, keep = got.view(torch.uint8), [0, 2, 5]
+    assert torch.equal(g[keep], want.view(torch.uint8)[keep]) and torch.equal(gs[keep], ws[keep])
+    assert ((g[3] & 0x7F) == 0x7F).all()
+    zero = torch.zeros(K, dtype=torch.uint8, device="cuda")
+    for row, at in ((1, 5), (4, 7)):
+        zero[at] = 0x7F
+        assert torch.equal(g[row] & 0x7F, zero)
+        zero[at] = 0
