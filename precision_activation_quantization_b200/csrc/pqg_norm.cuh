@@ -110,7 +110,7 @@ __device__ __forceinline__ float inverse_root(double v) {
     for (int i = 0; i < 2; ++i) d = fma(d, fma(half * d, d, 0.5), d);
     const float r = static_cast<float>(
         __hiloint2double(__double2hiint(d) - ((k / 2) << 20), __double2loint(d)));
-    return hi > 0x7FF00000 ? __int_as_float(0x7FFFFFFF) : r;   // a NaN; infinity gives 0
+    return v == v ? r : __int_as_float(0x7FFFFFFF);   // a NaN of either sign; infinity gives 0
 }
 
 // Store the scale of group g of a row (the slot's first lane calls it; for the

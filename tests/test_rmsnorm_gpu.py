@@ -21,6 +21,9 @@ KINDS = [("e4m3", "fp32", "row", 128), ("e4m3", "fp32", "col", 64), ("int8", "fp
          ("e2m1", "e4m3", "tile128x4", 16), ("e2m1", "e4m3", "col", 16)]
 
 
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
 def rows(M, K, seed, in_dtype):
     """Rows of unequal magnitude with outliers, zeros and an all-zero row."""
     rng = np.random.default_rng(seed)
@@ -240,3 +243,25 @@ def test_infinities_and_nans_stay_in_their_rows(K, scale_fmt):
         zero[at] = 0x7F
         assert torch.equal(g[row] & 0x7F, zero)
         zero[at] = 0
+
+
+@pytest.mark.parametrize("in_dtype,bits", [("bf16", 0x7FC0), ("bf16", 0xFFC0), ("bf16", 0x7F81), ("bf16", 0xFF81),
+                                           ("fp16", 0x7E00), ("fp16", 0xFE00)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_a_nan_of_either_sign_spoils_its_row(in_dtype, bits, residual):
+    """Also NaNs with the sign bit set (0xFFC0 is what a host's 0 / 0 leaves) and signalling
+    ones; with groups and per token, where few and where many rows split a row differently."""
+    for M, K in ((4, 256), (3, 7168), (1100, 1024)):
+        x = torch.randn(M, K, device="cuda").to(DT[in_dtype])
+        r = torch.randn(M, K, device="cuda").to(DT[in_dtype]) if residual else None
+        w = torch.rand(K, device="cuda").to(DT[in_dtype]) + 0.5
+        for scale_fmt in ("fp32", "ue8m0"):
+            for group in (128, K):
+                kw = dict(scale_fmt=scale_fmt, group=group)
+                want, ws, _ = pqg.rmsnorm_quant(x, w, r, **kw)
+                bad = x.clone()
+                bad.view(torch.int16)[1, K - 3] = bits - (1 << 16) if bits >> 15 else bits
+                got, gs, _ = pqg.rmsnorm_quant(bad, w, r, **kw)
+                g, keep = got.view(torch.uint8), [i for i in range(M) if i != 1]
+                assert ((g[1] & 0x7F) == 0x7F).all(), (M, K, kw)
+                assert torch.equal(g[keep], want.view(torch.uint8)[keep]) and torch.equal(gs[keep], ws[keep])
