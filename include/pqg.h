@@ -413,7 +413,8 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
  * Keys, values and queries enter the products exactly, except that (MXFP4) a
  * group of values whose scale is 2^-27 or less of the largest one that the
  * same elements have met counts as zero, a group of keys with scale byte 0
- * too; keys' scales from 2^118 on may give a score that is not finite.  The
+ * too; keys' scales from 2^118 on may give a score that is not finite, and
+ * values from 2^80 on a result that is not where scores pass 2^22 in size.  The
  * softmax weights are rounded to 11 bits for the product with V; sums are in
  * fp32.  A row whose query holds a NaN has out and lse NaN, once it sees a
  * key; other rows are not touched by it.  Results do not depend

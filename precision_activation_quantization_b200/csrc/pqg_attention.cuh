@@ -249,6 +249,22 @@ __device__ __forceinline__ float key_power(uint32_t e) {
     return __uint_as_float(e << 23) * (1.0f / kKeyShift);
 }
 
+// A warp's values are summed under weights that sum to l, up to 2^46 over many keys: with
+// values from 2^82 on such sums overflow where the mean, which is wanted, does not.  A warp
+// that has met scales of 2^kHugeScale moves a power of two from its sums to m, which rounds
+// nothing: l is in [2^-14, 2^-13) then, so that the sums of below 2^11 parts of 4 warps are
+// below the largest value.  m is a whole number; one from 2^23 on cannot take the power, so
+// there the sums stay as they are.  Returns the power.
+constexpr uint32_t kHugeScale = 50;
+__device__ __forceinline__ float move_power(float &m, float &l) {
+    if (!(fabsf(m) < 8388608.0f)) return 1.0f;
+    const int e = static_cast<int>(__float_as_uint(l) >> 23 & 0xFFu) - 113;
+    const float f = __uint_as_float(static_cast<uint32_t>(max(127 - e, 1)) << 23);
+    m += static_cast<float>(e);
+    l *= f;
+    return f;
+}
+
 // A word's bytes [from, from + 4) of a tile, those at or past `end` zeroed.
 __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
     const int n = min(max(end - from, 0), 4);
@@ -289,8 +305,8 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // so warps never wait on one another before the join.  A tile's rows are laid out
 // so that the lanes of one load meet 32 different banks (row_at below).
 //
-// The reference m of a row's weights 2^(score - m) lies 7 below a maximum: weights
-// near it are 2^7, so that small ones keep their bits in binary16, and m moves only
+// The reference m of a row's weights 2^(score - m) is a whole number 7 below a maximum:
+// weights near it are 2^7, so that small ones keep their bits in binary16, and m moves only
 // when a score exceeds it by 15, so that most tiles neither reduce a maximum across
 // lanes nor rescale.
 //
@@ -741,7 +757,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1)
                             top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], o));
-                        const float next = fmaxf(m[nt][k], top[k] - 7.0f);
+                        const float next = fmaxf(m[nt][k], floorf(top[k]) - 7.0f);
                         const float fade = ex2_approx(m[nt][k] - next);
                         m[nt][k] = next;
                         l[nt][k] *= fade;
@@ -844,11 +860,28 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
     // -- join the block's warps ----------------------------------------------------------
     const float grain = G == 16 ? 1.0f : exp2f(static_cast<float>(vref) - 139.0f);
 #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) l[nt][k] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][k], o);
+    if (G == 32 && __any_sync(0xFFFFFFFFu, vref >= 127u + kHugeScale)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float f = move_power(m[nt][k], l[nt][k]);
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    acc[i][nt][k] *= f;
+                    acc[i][nt][k + 2] *= f;
+                }
+            }
+    }
+#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l[nt][k] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][k], o);
             const uint32_t r = nt * kTileRows + 2u * tig + k;
             if (gid == 0) {
                 smem.stats[warp][r][0] = m[nt][k];

@@ -191,6 +191,22 @@ def test_scales_near_the_ends():
     check([200], 1, 9, 1, 256, 16, "mxfp4", "bf16", spread=(1, 8), sm_scale=1.0, q_size=2.0 ** 112)
 
 
+@pytest.mark.parametrize("lens", [[128, 100, 1], [5000, 30000], [2000] * 700])
+def test_huge_values_of_many_keys(lens):
+    """All keys alike and values up to 2^118: their sum is no fp32 number, their mean is.  In
+    whole units, in few and in many units that are split.  Values of one sign, so that the
+    mean is as large as they are."""
+    c, table = build(lens, 64, 1, 64, "mxfp4", spread=(240, 243))
+    c.v_codes.bitwise_and_(0x77)
+    c.k_scales.fill_(127)
+    q = torch.zeros(len(lens), 2, 64, device="cuda", dtype=torch.bfloat16)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = pqg.kv_attention(q, c, table, n, return_lse=True)
+    want = reference(q, c, table, lens, 1, 0.125)
+    assert want[0].amax() > 2.0 ** 114
+    compare(out, lse, want, "bf16", lens)
+
+
 @pytest.mark.parametrize("sign", [-1.0, 1.0])
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 def test_huge_scores(fmt, sign):
