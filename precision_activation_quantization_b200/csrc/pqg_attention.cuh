@@ -750,8 +750,9 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                 float top[2];
                 top[0] = fmaxf(fmaxf(score[0].x, score[1].x), fmaxf(score[2].x, score[3].x));
                 top[1] = fmaxf(fmaxf(score[0].y, score[1].y), fmaxf(score[2].y, score[3].y));
+                // (the difference, which is exact for near numbers: m + 15 is not for a huge m)
                 if (__any_sync(0xFFFFFFFFu,
-                               top[0] > m[nt][0] + 15.0f || top[1] > m[nt][1] + 15.0f)) {
+                               top[0] - m[nt][0] > 15.0f || top[1] - m[nt][1] > 15.0f)) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
 #pragma unroll

@@ -191,6 +191,31 @@ def test_scales_near_the_ends():
     check([200], 1, 9, 1, 256, 16, "mxfp4", "bf16", spread=(1, 8), sm_scale=1.0, q_size=2.0 ** 112)
 
 
+@pytest.mark.parametrize("e", [22, 24, 25, 26, 27, 28, 30])
+def test_scores_as_coarse_as_the_weights_range(e):
+    """Scores of about 2^e in log2 units, whose fp32 neighbours are 2^(e - 23) apart: the later keys
+    are one, two or three of those above the earlier ones, and no weight leaves binary16.
+
+    Every score is exact, so compare()'s error of the scores is 0: of an element's product 4 q_0 or
+    q_32 each is the only one of its group, a power of two (times 1, 2 or 3) within 24 bits of
+    the other; and fp32(ln 2) times log2(e), rounded to fp32, is 1."""
+    L, B, H = 1024, 100, 8                                # a block takes several pieces of a unit
+    c, table = build([L] * B, 64, H, 64, "mxfp4")
+    c.k_scales.fill_(127)
+    c.k_codes.zero_()
+    c.k_codes[..., 0] = 0x06                              # 4
+    for b in range(B):
+        c.k_codes[table[b, 8:16].long(), :, :, 16] = 0x02     # 1, of keys 512 and on
+    q = torch.zeros(B, 2 * H, 64, device="cuda", dtype=torch.bfloat16)
+    q[..., 0] = 2.0 ** (e - 2)
+    q[..., 32] = (2.0 ** (e - 23) * (1 + torch.arange(B, device="cuda") % 3))[:, None].bfloat16()
+    n = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    sm = float(np.float32(np.log(2.0)))
+    out, lse = pqg.kv_attention(q, c, table, n, sm_scale=sm, return_lse=True)
+    want = reference(q, c, table, [L] * B, 1, sm)
+    compare(out, lse, want[:3] + (torch.zeros_like(want[3]),), "bf16", [L])
+
+
 @pytest.mark.parametrize("lens", [[128, 100, 1], [5000, 30000], [2000] * 700])
 def test_huge_values_of_many_keys(lens):
     """All keys alike and values up to 2^118: their sum is no fp32 number, their mean is.  In
