@@ -415,8 +415,9 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
  * same elements have met counts as zero, a group of keys with scale byte 0
  * too; keys' scales from 2^118 on may give a score that is not finite, and
  * values from 2^80 on a result that is not where scores pass 2^22 in size.  The
- * softmax weights are rounded to 11 bits for the product with V; sums are in
- * fp32.  A row whose query holds a NaN has out and lse NaN, once it sees a
+ * softmax weights are rounded for the product with V, to 11 bits or by up to
+ * 2^-36 of the row's largest weight where that is more; the sum that divides
+ * them is of the weights as they were.  Sums are in fp32.  A row whose query holds a NaN has out and lse NaN, once it sees a
  * key; other rows are not touched by it.  Results do not depend
  * on anything but the arguments (no atomics), max_len and the number of the
  * device's SMs included.

@@ -249,6 +249,9 @@ __device__ __forceinline__ float key_power(uint32_t e) {
     return __uint_as_float(e << 23) * (1.0f / kKeyShift);
 }
 
+// A row's reference when set, below its maximum, and where it rises (2^kHigh fits binary16).
+constexpr float kBelow = 11.0f, kHigh = 15.0f;
+
 // A warp's values are summed under weights that sum to l, up to 2^46 over many keys: with
 // values from 2^82 on such sums overflow where the mean, which is wanted, does not.  A warp
 // that has met scales of 2^kHugeScale moves a power of two from its sums to m, which rounds
@@ -287,7 +290,8 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // different scales, so they are taken relative to a reference, 12 binades above 1: the
 // largest scale so far of the lane's elements.  A group whose scale is 2^-27 of the
 // reference or less counts as zero.  A query row is scaled by a power of two into
-// [2^14, 2^15).  Only the weights p are rounded, to binary16's 11 bits.
+// [2^14, 2^15).  Only the weights p are rounded: to binary16's 11 bits,
+// or by 2^-36 of the row's largest where that is more (see the reference m below).
 //
 // Layout.  A warp takes 32 keys at a time; tokens are M of the first product, so
 // that 8 query rows (N) cost no more tensor work than one.  The order of a sum's
@@ -305,10 +309,13 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // so warps never wait on one another before the join.  A tile's rows are laid out
 // so that the lanes of one load meet 32 different banks (row_at below).
 //
-// The reference m of a row's weights 2^(score - m) is a whole number 7 below a maximum:
-// weights near it are 2^7, so that small ones keep their bits in binary16, and m moves only
-// when a score exceeds it by 15, so that most tiles neither reduce a maximum across
-// lanes nor rescale.
+// The reference m of a row's weights 2^(score - m) is a whole number, kBelow to kBelow + 1
+// below a maximum when it is set, and rises when a score exceeds it by kHigh, so that most
+// tiles neither reduce a maximum across lanes nor rescale.  Weights below 2^-14 lose bits in
+// binary16, those below 2^-25 all of them: the error is 2^-25 at most where the row's largest
+// weight is 2^11 or more, 2^-36 of it.  A larger kBelow would reach further down but rise
+// more often: 13 costs the 64 sequences below 0.6 % and 131072 keys 0.8 %, 11 0.3 and 0.3 %,
+// against 7.
 //
 // Measured.  64 ragged sequences of up to 8192 keys, 32 query and 8 key heads of 128:
 // 348 MB of MXFP4 in 79 us (4.4 TB/s), 367 MB of NVFP4 in 75 us (4.9); one sequence
@@ -752,13 +759,14 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                 top[1] = fmaxf(fmaxf(score[0].y, score[1].y), fmaxf(score[2].y, score[3].y));
                 // (the difference, which is exact for near numbers: m + 15 is not for a huge m)
                 if (__any_sync(0xFFFFFFFFu,
-                               top[0] - m[nt][0] > 15.0f || top[1] - m[nt][1] > 15.0f)) {
+                               top[0] - m[nt][0] > kHigh || top[1] - m[nt][1] > kHigh)) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1)
                             top[k] = fmaxf(top[k], __shfl_xor_sync(0xFFFFFFFFu, top[k], o));
-                        const float next = fmaxf(m[nt][k], floorf(top[k]) - 7.0f);
+                        // (rounded up: a huge top's neighbours may be 16 apart)
+                        const float next = fmaxf(m[nt][k], __fadd_ru(floorf(top[k]), -kBelow));
                         const float fade = ex2_approx(m[nt][k] - next);
                         m[nt][k] = next;
                         l[nt][k] *= fade;

@@ -191,6 +191,45 @@ def test_scales_near_the_ends():
     check([200], 1, 9, 1, 256, 16, "mxfp4", "bf16", spread=(1, 8), sm_scale=1.0, q_size=2.0 ** 112)
 
 
+def sink(B, L, H, fmt, at, gap, v_byte, D=64, P=64):
+    """Sequences of L keys: key ``at`` has a score 2^gap above all the others, which are alike,
+    and values of zero; the others' values are all 1 under the scale v_byte.  Returns (cache, table,
+    sm_scale) for queries of one 1 and zeros."""
+    c, table = build([L] * B, P, H, D, fmt)
+    c.k_codes.zero_()
+    c.k_scales.fill_(127 if fmt == "mxfp4" else 0x38)     # 1 (under g for nvfp4)
+    c.v_scales.fill_(v_byte)
+    c.v_codes.fill_(0x22)
+    pages, off = table[:, at // P].long(), at % P
+    c.v_codes[pages, :, off] = 0
+    c.k_codes[pages, :, off, 0] = 0x02
+    return c, table, gap * np.log(2.0) * (1.0 if fmt == "mxfp4" else G_SCALE[0])
+
+
+@pytest.mark.parametrize("fmt,v_byte", [("mxfp4", 160), ("nvfp4", 0x7E)])
+@pytest.mark.parametrize("gap", [20.0, 30.4, 33.0])
+@pytest.mark.parametrize("B,L,H,at", [(1, 131072, 1, 0), (1, 131072, 1, 131071), (1, 500, 1, 40),
+                                      (100, 1024, 8, 0), (100, 1024, 8, 700)])
+def test_a_tail_far_below_one_key_keeps_its_weight(fmt, v_byte, gap, B, L, H, at):
+    """One key takes nearly all weight and has values of zero: the result is the tail's, whose
+    weights are 2^-20 to 2^-33.  Each is off by 2^-36 of the largest, whose weight is below 1, and all
+    values of the tail are alike: 2^-36 (L - 1) v is added to compare()'s bound.  Few units, cut into
+    pieces, and many, where the warp that has met the large key takes a quarter of the tail too."""
+    c, table, sm = sink(B, L, H, fmt, at, gap, v_byte)
+    n = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    v = float(values(c.v_codes[:1], c.v_scales[:1], fmt, G_SCALE[1]).max())
+    for group in (1, 12):
+        q = torch.zeros(B, group * H, 64, device="cuda", dtype=torch.bfloat16)
+        q[..., 0] = 1.0
+        out, lse = pqg.kv_attention(q, c, table, n, sm_scale=sm, return_lse=True)
+        wo, wl, absv, err = reference(q, c, table, [L] * B, 1, sm)
+        tol = (2.0 ** -11 + 2.0 ** -20 + 2 * err[..., None] + 2 * L * 2.0 ** -24) * absv + 2.0 ** -36 * (L - 1) * v
+        tol = tol + 2.0 ** -8 * (wo + tol)
+        assert ((out.double() - wo).abs() <= tol).all(), (float(out[0, 0, 0]), float(wo[0, 0, 0]))
+        assert (wo > 0.8 * (L - 1) * v * 2.0 ** -gap).all() and (tol < 0.2 * wo).all()
+        assert ((lse.double() - wl).abs() <= err + L * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -22 * wl.abs()).all()
+
+
 @pytest.mark.parametrize("e", [22, 24, 25, 26, 27, 28, 30])
 def test_scores_as_coarse_as_the_weights_range(e):
     """Scores of about 2^e in log2 units, whose fp32 neighbours are 2^(e - 23) apart: the later keys
