@@ -410,17 +410,22 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
  *          pqg_kv_attention_workspace(...) bytes for the same arguments,
  *          16-byte aligned (NULL when that is 0).  Its contents are dead
  *          after the call; calls that may run at the same time need one each.
- * Keys, values and queries enter the products exactly, except that (MXFP4) a
- * group of values whose scale is 2^-27 or less of the largest one that the
- * same elements have met counts as zero, a group of keys with scale byte 0
- * too; keys' scales from 2^118 on may give a score that is not finite, and
- * values from 2^80 on a result that is not where scores pass 2^22 in size.  The
- * softmax weights are rounded for the product with V, to 11 bits or by up to
- * 2^-36 of the row's largest weight where that is more; the sum that divides
- * them is of the weights as they were.  Sums are in fp32.  A row whose query holds a NaN has out and lse NaN, once it sees a
- * key; other rows are not touched by it.  Results do not depend
- * on anything but the arguments (no atomics), max_len and the number of the
- * device's SMs included.
+ * Precision.  Sums are in fp32.  Keys and values enter the products exactly,
+ * except that (MXFP4) a group of keys with scale byte 0 counts as zero, and so
+ * does a group of values whose scale is 2^-27 or less of the largest one of
+ * the same elements among the sequence's keys, those that a row does not see
+ * included.  An element of a query is off by up to 2^-39 of the largest one
+ * of its row (and head), which is exact down to 2^-31 (bf16) or 2^-28 (fp16)
+ * of it.  The softmax weights are rounded for the product with V, to 11 bits
+ * or by up to 2^-36 of the row's largest weight where that is more; the sum
+ * that divides them is of the weights as they were.  Keys' scales from 2^118
+ * on may give a score that is not finite, and values from 2^80 on a result
+ * that is not where scores pass 2^22 in size.  A row whose query holds a NaN
+ * has out and lse NaN, once it sees a key; other rows are not touched by it.
+ * Results are the same for the same arguments (no atomics), max_len and the
+ * number of the device's SMs included.  The other sequences of a call are
+ * among them: how the keys are split goes by all lengths, so the last bits of
+ * a sequence may differ from those of a call without its neighbours.
  */
 PQG_API int pqg_kv_attention(const pqg_kv_cache *cache, const void *q, int64_t q_stride,
               const int32_t *page_table, int64_t table_stride, int64_t max_pages,

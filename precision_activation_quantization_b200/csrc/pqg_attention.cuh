@@ -281,7 +281,7 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // Mathematics.  With c_jd the 4-bit code of key j, s_jg its scale and q the
 // query, score_j = sum_g sum_{d in g} q_d (c_jd s_jg); out = sum_j p_j (c_jd
 // s_jg) / sum_j p_j.  Both products run on the tensor cores in binary16 with
-// fp32 sums, and their operands are exact: a code has 2 significant bits and an
+// fp32 sums.  Keys and values are exact there: a code has 2 significant bits and an
 // E4M3 scale 4, so their product is a binary16 number.  A UE8M0 scale has a
 // wider range than binary16.  Keys: the codes alone are multiplied, a group (two steps
 // of 16 elements) at a time, and fp32 sums take the group's sum times its power: one
@@ -289,9 +289,10 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // (82.6 -> 82.0 us for the 64 sequences below).  Values: a sum runs over keys of
 // different scales, so they are taken relative to a reference, 12 binades above 1: the
 // largest scale so far of the lane's elements.  A group whose scale is 2^-27 of the
-// reference or less counts as zero.  A query row is scaled by a power of two into
-// [2^14, 2^15).  Only the weights p are rounded: to binary16's 11 bits,
-// or by 2^-36 of the row's largest where that is more (see the reference m below).
+// reference or less counts as zero.  A query row is scaled by a power of two so that its
+// largest element is in [2^14, 2^15): elements of 2^-14 and more are exact, smaller ones off by
+// 2^-25 at most, 2^-39 of the largest.  The weights p are rounded to binary16's 11 bits, or by
+// 2^-36 of the row's largest where that is more (see the reference m below).
 //
 // Layout.  A warp takes 32 keys at a time; tokens are M of the first product, so
 // that 8 query rows (N) cost no more tensor work than one.  The order of a sum's

@@ -185,6 +185,34 @@ def test_scales_far_apart():
     check([200], 1, 4, 1, 128, 16, "mxfp4", "fp16", spread=(118, 127), q_size=20000.0, sm_scale=1e-6)
 
 
+@pytest.mark.parametrize("in_dtype,fmt,wide", [("bf16", "mxfp4", 24), ("bf16", "mxfp4", 30), ("fp16", "mxfp4", 20),
+                                               ("bf16", "nvfp4", 12), ("fp16", "nvfp4", 12)])
+def test_queries_of_unequal_elements(in_dtype, fmt, wide):
+    """The first group's query elements are 2^wide times the others', its keys' scales as much
+    smaller, so that all groups weigh alike.  An element is off by 2^-39 of the row's largest, so a
+    score by sm_scale 2^-39 max |q| sum_d |K_d| more than compare()'s bound has."""
+    D, G, lens = 64, ref.GROUP[fmt], [300, 31]
+    c, table = build(lens, 32, 2, D, fmt, spread=(125, 128))
+    if fmt == "mxfp4":
+        c.k_scales[:, :, 0] -= torch.where(c.k_scales[:, :, 0] < 0xFF, wide, 0).to(torch.uint8)
+    else:                                                  # 2^-6, against 2^6 and more
+        c.k_scales[:, :, 0], c.k_scales[:, :, 1:] = 0x08, 0x68
+    q = torch.randn(2, 8, D, device="cuda")
+    q[..., :G] *= 2.0 ** wide
+    q = (q * (2.0 ** -8 if in_dtype == "fp16" else 1.0)).to(DT[in_dtype])
+    sm = 2.0 ** 5 if in_dtype == "fp16" and fmt == "mxfp4" else 0.125
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = pqg.kv_attention(q, c, table, n, sm_scale=sm, return_lse=True)
+    want = list(reference(q, c, table, lens, 1, sm))
+    for b, length in enumerate(lens):
+        pg = table[b, :-(-length // 32)].long()
+        k = values(c.k_codes[pg], c.k_scales[pg], fmt, G_SCALE[0]).transpose(0, 1).flatten(1, 2)[:, :length]
+        size = k.abs().sum(-1).amax(-1).repeat_interleave(4)
+        want[3][b] += sm * 2.0 ** -39 * q[b].double().abs().amax(-1) * size
+    assert want[3].max() < 0.2
+    compare(out, lse, want, in_dtype, lens)
+
+
 def test_scales_near_the_ends():
     """MXFP4 keys' scales up to 2^117 (with codes and queries: sums of 2^124), and down to 2^-126."""
     check([200], 1, 4, 1, 64, 32, "mxfp4", "bf16", spread=(238, 245), sm_scale=1.0, q_size=2.0 ** -116)
