@@ -10,8 +10,6 @@
 namespace pqg {
 namespace {
 
-constexpr uint32_t kManyRows = 1024;
-
 template <typename In, Kind KIND, int SLOTS, bool PER_TOKEN>
 cudaError_t launch_norm_variant(const NormParams &p, int warps, cudaStream_t stream) {
     auto kernel = rmsnorm_quant_kernel<In, KIND, SLOTS, PER_TOKEN>;
@@ -39,15 +37,30 @@ cudaError_t launch_norm_variant(const NormParams &p, int warps, cudaStream_t str
     return launch(kernel, ctas, warps * 32, smem, stream, p);
 }
 
+// Whether a per-token call of rows of 2 to 8 units takes half the warps with twice the
+// elements: a row's two reductions take less then, but fewer loads are in flight.  INT8, us
+// with all and with half the warps:
+//                     without a residual              with one
+//   8 units (K 4096)  512 rows 3.6 / 3.4 (128: 2.6 /  768 rows 5.0 / 4.8, 1024 6.5 / 5.9, 2048
+//                     2.8), 2048 9.4 / 7.5, 12288     12.8 / 12.7, 2560 14.6 / 15.2, 8192
+//                     47.6 / 39.9                     39.6 / 41.7
+//   4, 5 units        1536 rows 4.1 / 4.3, 2048 5.0 / 1024 rows 3.6 / 4.0, 2048 6.1 / 6.1,
+//   (K 2048)          5.0, 2560 6.2 / 5.7             6144 15.9 / 17.0
+//   2 units (K 1024)  1024 rows 3.0 / 3.3, 4096       1024 rows 3.1 / 3.4, 6144 9.6 / 12.0
+//                     6.0 / 7.0
+// With groups there is one reduction, and all warps are as fast or faster ([8192, 4096]
+// 40.3 / 40.9).
+bool half_the_warps(int units, uint32_t M, bool residual) {
+    if (units >= 7) return M >= 768 && (!residual || M < 2048);
+    return units >= 4 && M >= 2048 && !residual;
+}
+
 template <typename In, Kind KIND, bool PER_TOKEN>
 cudaError_t launch_norm_slots(const NormParams &p, cudaStream_t stream) {
     // a row is units of 32 lanes x 16 elements; a warp takes 1, 2 or 4 of them, so that
     // 8 warps are enough and as few of them as may be idle (K = 7168: 7 warps x 2)
     const int units = static_cast<int>((p.K / 16u + 31u) / 32u);
-    // Per-token calls of many rows take half the warps with twice the elements: the row's
-    // two reductions weigh more there ([8192, 4096] 32.8 -> 27.8 us); with groups, and
-    // for few rows, more warps are as fast or faster ([8192, 4096] 40.3 against 40.9).
-    if (PER_TOKEN && units > 1 && units <= 16 && p.M >= kManyRows)
+    if (PER_TOKEN && units <= 8 && half_the_warps(units, p.M, p.residual != nullptr))
         return launch_norm_variant<In, KIND, 2, PER_TOKEN>(p, (units + 1) / 2, stream);
     if (units <= 8) return launch_norm_variant<In, KIND, 1, PER_TOKEN>(p, units, stream);
     if (units <= 16)

@@ -97,6 +97,12 @@ def test_sizes_per_token(M, K):
     check(M, K, ("int8", "fp32", "row", "K"), "fp16", residual=False, seed=K)
 
 
+@pytest.mark.parametrize("M,K,residual", [(767, 4096, False), (768, 4096, True), (2047, 3840, True), (2048, 3840, True),
+                                          (2047, 2048, False), (2048, 2064, False), (2100, 2048, True)])
+def test_per_token_around_the_choices_of_warps(M, K, residual):
+    check(M, K, ("int8", "fp32", "row", "K"), residual=residual, seed=K)
+
+
 @pytest.mark.parametrize("M,K", [(1, 32), (4, 96), (131, 416), (1, 16384), (3, 8224), (1600, 544)])
 def test_sizes_groups(M, K):
     check(M, K, ("e4m3", "ue8m0", "packed", 32), seed=K)
