@@ -53,9 +53,12 @@ int make_plan(const CacheView &c, int64_t max_pages, int64_t B, int64_t q_len, i
     return PQG_OK;
 }
 
-// Query rows from which the join takes a warp per row (64 sequences x 64 heads: 58.1 ->
-// 53.7 us of the whole call; 4 x 32 rows of a long context lose, 23.9 -> 30.4 us).
-constexpr int64_t kManyJoins = 1024;
+// Query rows from which the join takes a warp per row rather than a block (32 query and 8 key
+// heads of 128, MXFP4; us of the whole call with a block and with a warp, for sequences of up
+// to 600, 2000 and 16384 keys: 128 rows 7.5 / 7.2, 7.9 / 8.1, 18.7 / 19.7; 256 rows 8.1 / 7.7,
+// 9.1 / 9.2, 26.0 / 26.2; 512 rows 9.9 / 8.9, 13.5 / 12.3, 46.6 / 45.8; 2048 rows 20.7 / 16.3,
+// 33.1 / 28.4, 139.5 / 133.7; 64 rows of 131072 keys 36.6 / 42.0).
+constexpr int64_t kManyJoins = 512;
 
 template <typename In, int G, int D, int NT>
 cudaError_t launch_rows(const AttentionParams &p, const Plan &plan, cudaStream_t stream,

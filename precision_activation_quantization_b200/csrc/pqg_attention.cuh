@@ -376,7 +376,9 @@ struct AttentionShape {
 // blocks the kernels take 119 to 128 registers; 5 blocks spill or lose more to the
 // schedule than the warps bring (64 sequences up to 8192 keys, 84.8 against 90.6 us),
 // 3 are slower too (87.3).  16 rows of a head of 128 need 3 (32 sequences with 16 query
-// heads per key head: 86.3 -> 79.4 us against 2).
+// heads per key head: 86.3 -> 79.4 us against 2).  16 rows of a head of 64 need 4 (64 sequences
+// up to 8192 keys with 16 query heads per key head: 48.4 -> 47.3 us MXFP4, 45.2 -> 44.5 NVFP4
+// against 3; 16 up to 2000 keys: 11.3 -> 9.7).
 __host__ __device__ constexpr int attention_blocks(int D, int NT) {
     return D == 128 && NT == 2 ? 3 : 4;
 }
