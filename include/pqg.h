@@ -267,20 +267,23 @@ PQG_API int pqg_quant_varlen(const void *in, void *out, void *scales,
 /*
  * pqg_rmsnorm_quant — residual addition, root-mean-square norm and
  * quantization of M rows of K elements in one pass: the producer of a
- * block-scaled GEMM's input, without a 16-bit norm output in memory.  The
- * scale rules, codes and layouts are pqg_quant's (and pqg_quant_nvfp4's).
- * Per row:
+ * block-scaled GEMM's input, without a 16-bit norm output in memory.  Codes,
+ * layouts and the rules of byte scales are pqg_quant's (and
+ * pqg_quant_nvfp4's); fp32 scales have a rule of their own.  Per row:
  *   h_i  = x_i + residual_i, one fp32 addition rounded to in_dtype (h = x
  *          without a residual); stored to residual_out when it is not NULL
  *   inv  = 1 / sqrt(sum_i h_i^2 / K + eps), evaluated in 64 bits and rounded
- *          once to fp32.  A 64-bit sum does not depend on the order of its
- *          terms at fp32 precision, so a row's codes do not depend on how
- *          many rows the call has or on how a row is split
+ *          once to fp32
  *   y_i  = (h_i * inv) * weight_i, two fp32 roundings; y is what is quantized
  *          and is not rounded to 16 bits
  *   FP32 scales: s = amax * c, one fp32 multiplication by the fp32 constant c
- *          nearest 1 / 448 (E4M3) or 1 / 127 (INT8); codes from fp32(y / s)
- * Codes, scales and h are bit-identical to that definition.
+ *          nearest 1 / 448 (E4M3) or 1 / 127 (INT8), at most an ulp from the
+ *          quotient that pqg_quant stores; codes from fp32(y / s)
+ * Codes, scales and h are bit-identical to that definition, however many rows
+ * the call has, but for rows whose inv lies within a few units of its 64 bits
+ * of the middle between two fp32 numbers, about one in 10^8: the order of the
+ * sum, which goes by the call's sizes, and a root that is right to the last
+ * bit or two of 53 then decide which of the two inv is.
  *
  * in       device [M][K] of in_dtype, 32-byte aligned.
  * residual device [M][K] of in_dtype or NULL, 32-byte aligned.

@@ -3,10 +3,10 @@
 //
 // Mathematics.  h = x + r (rounded to the input type), inv = 1 / sqrt(mean(h^2)
 // + eps), y = (h inv) w, and y is quantized by groups as in pqg_kernel.cuh.
-// The sum of squares is kept in 64 bits: its value, rounded to fp32 inside inv,
-// is then the same in whatever order the terms are added, so a row's codes do
-// not depend on the launch shape, and an independent implementation meets the
-// same codes bit for bit.  One conversion and one 64-bit FMA per element fit
+// The sum of squares is kept in 64 bits: the order of its terms then moves inv, an
+// fp32 number, only where it lies within some 2^-50 of the middle between two of
+// them, about one row in 10^8.  All other rows have the same codes whatever the launch
+// shape, and an independent implementation meets them bit for bit.  One conversion and one 64-bit FMA per element fit
 // beside the memory traffic (an SM streams about 3.5 elements per clock here,
 // and its 64-bit pipe takes many more).
 //
@@ -77,9 +77,9 @@ __device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b) {
 }
 
 // A group's scale.  The fp32 scales are amax times the fp32 constant nearest 1 /
-// FMAX, one rounding (at most an ulp from pqg_quant's quotient; y is not a
-// 16-bit value, so no unfused call gives the same bits anyway); the codes are
-// the rounding of fp32(y / s) for that s.  The other kinds as in make_scale.
+// FMAX, as this entry point defines them: one rounding, and at most an ulp from the
+// quotient that pqg_quant stores (make_scale).  The codes are the rounding of
+// fp32(y / s) for that s.  The other kinds as in make_scale.
 template <Kind KIND>
 __device__ __forceinline__ GroupScale make_norm_scale(float amax, const float *nv) {
     if constexpr (KIND == Kind::E4M3_FP32 || KIND == Kind::INT8_FP32) {
