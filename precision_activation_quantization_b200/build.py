@@ -25,6 +25,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpqg.so")
 BINDING = os.path.join(PKG, "_pqg_torch.so")
 BINDING_SRC = os.path.join(CSRC, "pqg_torch.cpp")
+BINDING_ABI = BINDING[:-3] + ".abi"   # the torch and python that BINDING was built for
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -89,12 +90,26 @@ def build(force: bool = False, verbose: bool = False, defines=(), out: str = LIB
     return out
 
 
+def binding_abi() -> str:
+    """What a built binding depends on beside its sources."""
+    import torch
+    return f"torch {torch.__version__}, {sysconfig.get_config_var('SOABI')}\n"
+
+
+def binding_up_to_date() -> bool:
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "pqg.h"), os.path.abspath(__file__)]
+    if not os.path.exists(BINDING) or not os.path.exists(BINDING_ABI):
+        return False
+    with open(BINDING_ABI, encoding="utf-8") as f:
+        if f.read() != binding_abi():
+            return False
+    return all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps)
+
+
 def build_binding(force: bool = False) -> str:
     """Compile _pqg_torch.so against the installed torch unless it is newer than
-    its sources."""
-    deps = [BINDING_SRC, os.path.join(INCLUDE, "pqg.h"), os.path.abspath(__file__)]
-    if (not force and os.path.exists(BINDING)
-            and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps)):
+    its sources and was built for the same torch and python."""
+    if not force and binding_up_to_date():
         return BINDING
     import torch
     home = os.path.dirname(os.path.abspath(torch.__file__))
@@ -112,6 +127,8 @@ def build_binding(force: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{res.stderr}")
     os.replace(tmp, BINDING)
+    with open(BINDING_ABI, "w", encoding="utf-8") as f:
+        f.write(binding_abi())
     return BINDING
 
 
