@@ -438,7 +438,9 @@ def _allocating_on(stream, device):
     if stream is None:
         return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(stream, device=device)
+        # (an ExternalStream of handle 0 would be a new stream, not the default one)
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
     return torch.cuda.stream(stream)
 
 

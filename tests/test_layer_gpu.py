@@ -113,3 +113,31 @@ def test_prefill_then_captured_decode_steps(fmt):
     k, v = pqg.kv_read(layer.cache, table, indptr, int(indptr[-1]))
     assert torch.isfinite(k).all() and (k.abs().amax(-1) > 0).all() and (v.abs().amax(-1) > 0).all()
     assert int(layer.cache.k_codes[-1].max()) == 0 and int(layer.cache.v_scales[-1].max()) == 0
+
+
+def test_a_stream_may_be_a_handle():
+    """Calls on streams given as numbers run there and allocate from their pools, the default stream's 0 included."""
+    side = torch.cuda.Stream()
+    dev = torch.device("cuda", torch.cuda.current_device())
+    for stream in (0, side.cuda_stream, side):
+        for current in (torch.cuda.default_stream(), torch.cuda.Stream()):
+            with torch.cuda.stream(current), pqg._allocating_on(stream, dev):
+                assert torch.cuda.current_stream().cuda_stream == getattr(stream, "cuda_stream", stream)
+    layer = Layer("mxfp4", 4)
+    x, r = (torch.randn(5, K, device="cuda").to(torch.bfloat16) for _ in range(2))
+    k = torch.randn(5, H, D, device="cuda").to(torch.bfloat16)
+    q = torch.randn(1, HQ, D, device="cuda").to(torch.bfloat16)
+    slots = torch.arange(5, dtype=torch.int32, device="cuda")
+    table = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    n = torch.tensor([5], dtype=torch.int32, device="cuda")
+    indptr = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    got = []
+    for stream in (None, 0, side.cuda_stream, side):
+        pqg.kv_write(layer.cache, k, k, slots, stream=stream)
+        got.append([*pqg.rmsnorm_quant(x, layer.n1, r, stream=stream),
+                    *pqg.kv_read(layer.cache, table, indptr, 5, stream=stream),
+                    pqg.kv_attention(q, layer.cache, table, n, stream=stream)])
+        torch.cuda.synchronize()
+    for other in got[1:]:
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got[0], other))
