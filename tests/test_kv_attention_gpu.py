@@ -136,6 +136,42 @@ def test_types_and_head_dims(D, fmt, in_dtype):
     check([300, 517], 1, 12, 3, D, 64, fmt, in_dtype, seed=2, strided=True)
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("in_dtype", ["bf16", "fp16"])
+def test_written_rows_against_the_oracle(fmt, in_dtype):
+    """Keys and values written by kv_write: the cache holds the oracle's codes, and three tokens'
+    attention over it is that of the oracle's values in numpy, within compare()'s bound."""
+    from test_rmsnorm_gpu import dev, host
+    lens, q_len, P, H, D = [37, 5], 3, 16, 2, 64
+    gs = torch.tensor(G_SCALE, device="cuda") if fmt == "nvfp4" else None
+    c = pqg.kv_allocate(6, P, H, D, fmt=fmt, global_scale=gs)
+    table = np.array([[4, 0, 2], [5, -1, -1]], np.int32)
+    rng = np.random.default_rng(3)
+    kv = [host(torch.from_numpy(rng.standard_normal((sum(lens), H, D)).astype(np.float32)).to(DT[in_dtype])) for _ in range(2)]
+    at = [(int(table[b, j // P]), j % P) for b, n in enumerate(lens) for j in range(n)]
+    slots = torch.tensor([p * P + o for p, o in at], dtype=torch.int32, device="cuda")
+    pqg.kv_write(c, dev(kv[0], in_dtype), dev(kv[1], in_dtype), slots)
+    q = torch.from_numpy(rng.standard_normal((len(lens) * q_len, 2 * H, D)).astype(np.float32)).to(DT[in_dtype])
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = pqg.kv_attention(q.cuda(), c, torch.from_numpy(table).cuda(), n, return_lse=True)
+    held = []
+    for bits, codes, g in zip(kv, (c.k_codes, c.v_codes), G_SCALE):
+        got, scales = ref.quantise(bits.reshape(-1, D), fmt, g, in_dtype)
+        rows = [ref.row(codes.cpu().numpy(), p, o, h) for p, o in at for h in range(H)]
+        assert (np.stack(rows) == got).all()
+        held.append(ref.held(got, scales, fmt, g).reshape(-1, H, D))
+    first = 0
+    for b, length in enumerate(lens):
+        k, v = (x[first:first + length] for x in held)
+        qb = q[b * q_len:(b + 1) * q_len].double().numpy()
+        wo, wl = ref.attention(qb, k, v, D ** -0.5)
+        big = np.abs(v).max(0).repeat(2, 0)[None]              # at least sum p |V|
+        err = np.abs(qb).sum(-1) * np.abs(k).max() * D ** -0.5 * (D + 8) * 2.0 ** -24
+        want = [torch.from_numpy(x).cuda() for x in (wo, wl, np.broadcast_to(big, wo.shape).copy(), err)]
+        compare(out[b * q_len:(b + 1) * q_len], lse[b * q_len:(b + 1) * q_len], want, in_dtype, [length])
+        first += length
+
+
 @pytest.mark.parametrize("group", [1, 2, 3, 5, 7, 8, 9, 12, 16, 33])
 def test_head_groups(group):
     check([65, 130], 1, 2 * group, 2, 128, 32, "mxfp4", "bf16", seed=group)
