@@ -162,6 +162,21 @@ def test_rows_do_not_depend_on_the_batch():
             assert torch.equal(a.view(torch.uint8), b[at:at + n].contiguous().view(torch.uint8))
 
 
+def test_rows_past_4_gb():
+    """Rows, codes and scales whose offsets pass 32 bits: as the same rows alone."""
+    M, K = 620_000, 7168                                  # 8.9 GB of rows, 4.4 GB of codes
+    x = torch.zeros(M, K, device="cuda", dtype=torch.bfloat16)
+    w = dev(rows(1, K, 5, "bf16")[0], "bf16")
+    at = [0, 299_593, 299_594, 599_186, 599_187, M - 1]   # also around 2^32 bytes of each
+    x[at] = dev(rows(len(at), K, 3, "bf16"), "bf16")
+    got = pqg.rmsnorm_quant(x, w, x, residual_out=x)
+    few = dev(rows(len(at), K, 3, "bf16"), "bf16")
+    want = pqg.rmsnorm_quant(few, w, few)
+    for a, b in zip(got, want):
+        assert torch.equal(a[at].view(torch.uint8), b.view(torch.uint8))
+    assert int((got[0][1:299_593].view(torch.uint8) & 0x7F).amax()) == 0   # a zero has its weight's sign
+
+
 def test_other_stream_graph_and_pdl_off():
     K, M = 2048, 24
     x, r = dev(rows(M, K, 6, "fp16"), "fp16"), dev(rows(M, K, 7, "fp16"), "fp16")
