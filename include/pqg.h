@@ -416,8 +416,8 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
  * Precision.  Sums are in fp32.  Keys and values enter the products exactly,
  * except that (MXFP4) a group of keys with scale byte 0 counts as zero, and so
  * does a group of values whose scale is 2^-27 or less of the largest one of
- * the same elements among the sequence's keys, those that a row does not see
- * included.  An element of a query is off by up to 2^-39 of the largest one
+ * the same elements among the keys that the row sees; keys that it does not
+ * see never touch it.  An element of a query is off by up to 2^-39 of the largest one
  * of its row (and head), which is exact down to 2^-31 (bf16) or 2^-28 (fp16)
  * of it.  The softmax weights are rounded for the product with V, to 11 bits
  * or by up to 2^-36 of the row's largest weight where that is more; the sum

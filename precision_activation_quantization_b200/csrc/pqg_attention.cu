@@ -64,8 +64,10 @@ template <typename In, int G, int D, int NT>
 cudaError_t launch_rows(const AttentionParams &p, const Plan &plan, cudaStream_t stream,
                         int *kernels) {
     *kernels = 1;
-    const cudaError_t err = launch(attention_kernel<In, G, D, NT>, plan.shares,
-                                   attention_warps(D) * 32, 0, stream, p);
+    auto kernel = attention_kernel<In, G, D, NT, false>;
+    if constexpr (G == 32)
+        if (p.q_len > 1u) kernel = attention_kernel<In, G, D, NT, true>;
+    const cudaError_t err = launch(kernel, plan.shares, attention_warps(D) * 32, 0, stream, p);
     if (err != cudaSuccess || !plan.split) return err;
     *kernels = 2;
     const int64_t rows = static_cast<int64_t>(p.B) * p.c.heads * p.rows;

@@ -231,6 +231,14 @@ __device__ __forceinline__ void load_shared(const uint8_t *p, uint32_t (&w)[N]) 
 // The larger half of a pair of 16-bit numbers.
 __device__ __forceinline__ uint32_t larger_half(uint32_t v) { return max(v & 0xFFFFu, v >> 16); }
 
+// The smallest of eight 16-bit numbers that is not 0 (0x10000 where all are).
+__device__ __forceinline__ uint32_t smallest_half(const uint32_t (&e)[4]) {
+    uint32_t low = 0xFFFFFFFFu;                // of e - 1, which 0 wraps around
+#pragma unroll
+    for (int x = 0; x < 4; ++x) low = __viaddmin_u16x2(e[x], 0xFFFFFFFFu, low);
+    return min(low & 0xFFFFu, low >> 16) + 1u;
+}
+
 // 2^(e - ref + 12) in binary16 for two UE8M0 bytes (in bits 0-7 and 16-23) that
 // are at most ref, which comes as reference2(ref); 0 where the power is below 2^-14.
 __device__ __forceinline__ uint32_t relative_power2(uint32_t e2, uint32_t ref2) {
@@ -260,7 +268,7 @@ constexpr float kBelow = 11.0f, kHigh = 15.0f;
 // there the sums stay as they are.  Returns the power.
 constexpr uint32_t kHugeScale = 50;
 __device__ __forceinline__ float move_power(float &m, float &l) {
-    if (!(fabsf(m) < 8388608.0f)) return 1.0f;
+    if (!(fabsf(m) < 8388608.0f) || l == 0.0f) return 1.0f;
     const int e = static_cast<int>(__float_as_uint(l) >> 23 & 0xFFu) - 113;
     const float f = __uint_as_float(static_cast<uint32_t>(max(127 - e, 1)) << 23);
     m += static_cast<float>(e);
@@ -289,7 +297,10 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // (82.6 -> 82.0 us for the 64 sequences below).  Values: a sum runs over keys of
 // different scales, so they are taken relative to a reference, 12 binades above 1: the
 // largest scale so far of the lane's elements.  A group whose scale is 2^-27 of the
-// reference or less counts as zero.  A query row is scaled by a power of two so that its
+// reference or less counts as zero.  With several new tokens some rows do not see the keys
+// of the last tiles, nor then any newer ones, and must not lose theirs to a large scale
+// there: such a tile adds its groups by rising scale, the reference raised by up to 26 in
+// between.  (In a kernel of its own: the loop, though not run, costs the others 1 to 4 %.)  A query row is scaled by a power of two so that its
 // largest element is in [2^14, 2^15): elements of 2^-14 and more are exact, smaller ones off by
 // 2^-25 at most, 2^-39 of the largest.  The weights p are rounded to binary16's 11 bits, or by
 // 2^-36 of the row's largest where that is more (see the reference m below).
@@ -385,7 +396,7 @@ __host__ __device__ constexpr int attention_blocks(int D, int NT) {
 
 // Query rows [tile * R, + R) of (sequence b, key/value head) over keys [k_begin, k_end)
 // of its n: written out when `whole`, else left at `place` of the workspace.
-template <typename In, int G, int D, int NT>
+template <typename In, int G, int D, int NT, bool MULTI>
 __device__ __forceinline__ void attend(const AttentionParams &p,
                                        typename AttentionShape<G, D, NT>::Shared &smem, uint32_t b,
                                        uint32_t head, uint32_t tile, uint32_t n, uint32_t k_begin,
@@ -605,6 +616,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                           now[1] < 0;
         auto body = [&](auto edge_tag) {
             constexpr bool EDGE = decltype(edge_tag)::value;
+            constexpr bool PASSES = EDGE && MULTI && G == 32;
             uint32_t vsc[VG][2];
 #pragma unroll
             for (int g = 0; g < VG; ++g)
@@ -795,6 +807,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
 
             // -- weighted values ------------------------------------------------------------
             uint32_t vs[VG][4];                    // scales of tokens x and x + 4 of this lane's 8
+            uint32_t e[4];                         // MXFP4: their exponents, 16 bits each
             if constexpr (G == 16) {
 #pragma unroll
                 for (int g = 0; g < VG; ++g) {
@@ -811,25 +824,53 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                 // scales of tokens x and x + 4, 16 bits each
                 const uint32_t first = __byte_perm(vsc[0][0], vsc[0][1], 0x5410);
                 const uint32_t last = __byte_perm(vsc[0][0], vsc[0][1], 0x7632);
-                uint32_t e[4] = {first & 0x00FF00FFu, (first >> 8) & 0x00FF00FFu,
-                                 last & 0x00FF00FFu, (last >> 8) & 0x00FF00FFu};
+                e[0] = first & 0x00FF00FFu, e[1] = (first >> 8) & 0x00FF00FFu;
+                e[2] = last & 0x00FF00FFu, e[3] = (last >> 8) & 0x00FF00FFu;
+            }
+            // once, or (PASSES) until no scale is left above the reference
+            bool again = false;
+            do {
+            if constexpr (G == 32) {
                 uint32_t top = __vimax3_u16x2(e[0], e[1], vref * 0x00010001u);
                 top = __vimax3_u16x2(e[2], e[3], top);
                 if (__any_sync(0xFFFFFFFFu, top != vref * 0x00010001u)) {
                     uint32_t next = larger_half(top);
                     next = max(next, __shfl_xor_sync(0xFFFFFFFFu, next, 1));
                     next = max(next, __shfl_xor_sync(0xFFFFFFFFu, next, 2));
-                    const float fade = ex2_approx(-static_cast<float>(next - vref));
+                    if constexpr (PASSES) {    // by no more than keeps the smallest scale
+                        uint32_t low = smallest_half(e);
+                        low = min(low, __shfl_xor_sync(0xFFFFFFFFu, low, 1));
+                        low = min(low, __shfl_xor_sync(0xFFFFFFFFu, low, 2));
+                        next = min(next, max(low + 26u, vref));
+                    }
+                    const uint32_t up = next - vref;
                     vref = next;
+                    // PASSES: in two steps, since no factor below 2^-126 is normal
+                    const float fade = ex2_approx(-static_cast<float>(PASSES ? up / 2u : up));
+                    const float rest =
+                        PASSES ? ex2_approx(-static_cast<float>(up - up / 2u)) : 1.0f;
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) acc[i][nt][k] *= fade;
+                            for (int k = 0; k < 4; ++k) {
+                                acc[i][nt][k] *= fade;
+                                if constexpr (PASSES) acc[i][nt][k] *= rest;
+                            }
                 }
+                if constexpr (PASSES) {
 #pragma unroll
-                for (int x = 0; x < 4; ++x) vs[0][x] = relative_power2(e[x], reference2(vref));
+                    for (int x = 0; x < 4; ++x) {
+                        const uint32_t taken = e[x] & __vcmpleu2(e[x], vref * 0x00010001u);
+                        vs[0][x] = relative_power2(taken, reference2(vref));
+                        e[x] ^= taken;         // those above the reference wait
+                    }
+                    again = __any_sync(0xFFFFFFFFu, (e[0] | e[1] | e[2] | e[3]) != 0u);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) vs[0][x] = relative_power2(e[x], reference2(vref));
+                }
             }
             uint32_t vraw[8][VW];
 #pragma unroll
@@ -860,6 +901,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
                                      odd[1][i], weights[nt][2 * ks2], weights[nt][2 * ks2 + 1]);
                 }
             }
+            } while (PASSES && again);
         };
         if (edge) body(std::true_type{});
         else body(std::false_type{});
@@ -870,7 +912,7 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
     __syncwarp();                              // the buffers are free for the join
 
     // -- join the block's warps ----------------------------------------------------------
-    const float grain = G == 16 ? 1.0f : exp2f(static_cast<float>(vref) - 139.0f);
+    float grain = G == 16 ? 1.0f : exp2f(static_cast<float>(vref) - 139.0f);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -882,13 +924,15 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const float f = move_power(m[nt][k], l[nt][k]);
+                // (with grain at once: sums of values far below the reference are small)
+                const float f = move_power(m[nt][k], l[nt][k]) * grain;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     acc[i][nt][k] *= f;
                     acc[i][nt][k + 2] *= f;
                 }
             }
+        grain = 1.0f;
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -939,7 +983,8 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
     }
 }
 
-template <typename In, int G, int D, int NT>
+// MULTI: several new tokens of a sequence (it makes a difference with MXFP4 alone).
+template <typename In, int G, int D, int NT, bool MULTI>
 __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks(D, NT))
     attention_kernel(const __grid_constant__ AttentionParams p) {
     using Shape = AttentionShape<G, D, NT>;
@@ -956,7 +1001,7 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks(D, N
         // a share's first unit may have begun in another share, its last may end in one
         const uint32_t place = 2u * blockIdx.x + (share.at == first ? 0u : 1u);
         const uint32_t head = unit / p.row_tiles;
-        attend<In, G, D, NT>(p, smem, share.b, head, unit - head * p.row_tiles, n,
+        attend<In, G, D, NT, MULTI>(p, smem, share.b, head, unit - head * p.row_tiles, n,
                              piece * kPieceKeys, min(n, (piece + taken) * kPieceKeys),
                              taken == pieces, place);
         // the block that holds a unit's first piece says where its parts are: its own

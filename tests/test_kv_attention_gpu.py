@@ -405,6 +405,23 @@ def test_masked_queries_are_not_read_into_others():
     assert (got[:2] == 0).all() and torch.equal(got[2:], want[2:])
 
 
+@pytest.mark.parametrize("D,Hq", [(64, 2), (64, 24), (128, 8), (128, 24), (256, 8)])
+@pytest.mark.parametrize("q_len,newest,before", [(2, 90, 40), (5, 90, 40), (40, 90, 40), (3, 27, 26), (4, 125, 121), (150, 60, 30)])
+def test_hidden_values_do_not_touch_a_row(D, Hq, q_len, newest, before):
+    """The newest token's values are up to 2^125 times the others', and the one's before them
+    too: the rows of older tokens, which do not see them, are those of their own keys."""
+    H, P = 2, 16
+    lens = [q_len, 33 + q_len, 64, 100, 700, 3000]
+    c, table = build(lens, P, H, D, "mxfp4", seed=q_len)
+    for b, n in enumerate(lens):
+        for at, up in ((n - 1, newest), (n - 2, before)):
+            c.v_scales[int(table[b, at // P]), :, :, at % P] += up
+    q = torch.randn(len(lens) * q_len, Hq, D, device="cuda").to(torch.bfloat16)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = pqg.kv_attention(q, c, table, n, return_lse=True)
+    compare(out, lse, reference(q, c, table, lens, q_len, D ** -0.5), "bf16", lens)
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 def test_a_nan_query_spoils_its_own_row(fmt):
     """One head's row, in a whole unit and in one that is split; other rows keep their bits."""
