@@ -384,8 +384,9 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
 
 /*
  * pqg_kv_attention — attention of the last q_len tokens of B sequences over
- * the cache (decode: q_len = 1; several tokens: verification of drafts).  The
- * tokens' own keys and values are in the cache already.  With n = seq_lens[b],
+ * the cache (decode: q_len = 1; several tokens: verification of drafts; a
+ * chunk of some 200 tokens or more is faster with pqg_kv_read and a 16-bit
+ * attention).  The tokens' own keys and values are in the cache already.  With n = seq_lens[b],
  * clamped into [0, max_pages * page_size], token t of sequence b sees keys
  * j < n - (q_len - 1 - t):
  *   s_j = sm_scale * sum_d q_d K_jd,  out = sum_j softmax(s)_j V_j,

@@ -330,15 +330,20 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // against 7.
 //
 // Measured.  64 ragged sequences of up to 8192 keys, 32 query and 8 key heads of 128:
-// 348 MB of MXFP4 in 79 us (4.4 TB/s), 367 MB of NVFP4 in 75 us (4.9); one sequence
-// of 131072 keys, 151 MB, in 36.5 us.  HBM would take 53, 56 and 23.  What bounds it is
-// the mixture of one tensor instruction, four conversions and four binary16
-// multiplications that 16 keys x 16 elements need (without the last for MXFP4 keys):
-// each of the three alone takes 2.0 clocks of an SM, two of them 2.5 to 3.6, but all
-// together 5.0, at any occupancy.  With the copies left out the 64 sequences take 70 us:
-// weighted values 27, scores 21, softmax, loop and start 23; copies and softmax alone
-// take 60.  Blocks of 12 or 20 warps an SM are slower than 16, and moving the shifts to
-// the multiplier changes nothing.
+// 348 MB of MXFP4 in 79.4 us (4.4 TB/s), 367 MB of NVFP4 in 75.5 us (4.9); one sequence
+// of 131072 keys, 151 MB, in 36.5 us.  HBM would take 53, 56 and 23.  No pipe is full: of
+// the first call 62 % of the issue slots, 53 % of the ALU and 26 % of the tensor pipe are
+// busy, at 4 warps per scheduler.  A tile of 32 MXFP4 keys takes 616 warp instructions, of
+// which 128 convert codes, 64 multiply values by scales and 32 are products; the larger part
+// is addresses, reads of shared memory, interleaving, softmax and the loop.  A loop of one
+// product, four conversions and four multiplications alone takes 5 clocks of an SM (each kind
+// alone 2), which is half of what the long sequence takes.  With the copies left out the 64
+// sequences take 70 us: weighted values 27, scores 21, softmax, loop and start 23; copies and
+// softmax alone take 60.  Blocks of 12 or 20 warps an SM are slower than 16, and moving the
+// shifts to the multiplier changes nothing.
+//
+// Every 8 or 16 query rows read and decode the keys again, so that many new tokens run at
+// some 200 TFLOP/s (512 over 8192 keys, MXFP4: 332 us).
 
 // (A lane's tokens as rows of the first product's M: m-tile mt, rows gid and gid + 8
 // are tokens 4 gid + 2 mt and 4 gid + 2 mt + 1.)
