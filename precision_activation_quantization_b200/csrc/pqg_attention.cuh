@@ -300,10 +300,11 @@ __device__ __forceinline__ uint32_t keep_bytes(uint32_t w, int from, int end) {
 // reference or less counts as zero.  With several new tokens some rows do not see the keys
 // of the last tiles, nor then any newer ones, and must not lose theirs to a large scale
 // there: such a tile adds its groups by rising scale, the reference raised by up to 26 in
-// between.  (In a kernel of its own: the loop, though not run, costs the others 1 to 4 %.)  A query row is scaled by a power of two so that its
-// largest element is in [2^14, 2^15): elements of 2^-14 and more are exact, smaller ones off by
-// 2^-25 at most, 2^-39 of the largest.  The weights p are rounded to binary16's 11 bits, or by
-// 2^-36 of the row's largest where that is more (see the reference m below).
+// between.  (In a kernel of its own: the loop, though not run, costs the others 1 to 4 %.)
+// A query row is scaled by a power of two so that its largest element is in [2^14, 2^15):
+// elements of 2^-14 and more are exact, smaller ones off by 2^-25 at most, 2^-39 of the
+// largest.  The weights p are rounded to binary16's 11 bits, or by 2^-36 of the row's largest
+// where that is more (see the reference m below).
 //
 // Layout.  A warp takes 32 keys at a time; tokens are M of the first product, so
 // that 8 query rows (N) cost no more tensor work than one.  The order of a sum's
@@ -835,77 +836,78 @@ __device__ __forceinline__ void attend(const AttentionParams &p,
             // once, or (PASSES) until no scale is left above the reference
             bool again = false;
             do {
-            if constexpr (G == 32) {
-                uint32_t top = __vimax3_u16x2(e[0], e[1], vref * 0x00010001u);
-                top = __vimax3_u16x2(e[2], e[3], top);
-                if (__any_sync(0xFFFFFFFFu, top != vref * 0x00010001u)) {
-                    uint32_t next = larger_half(top);
-                    next = max(next, __shfl_xor_sync(0xFFFFFFFFu, next, 1));
-                    next = max(next, __shfl_xor_sync(0xFFFFFFFFu, next, 2));
-                    if constexpr (PASSES) {    // by no more than keeps the smallest scale
-                        uint32_t low = smallest_half(e);
-                        low = min(low, __shfl_xor_sync(0xFFFFFFFFu, low, 1));
-                        low = min(low, __shfl_xor_sync(0xFFFFFFFFu, low, 2));
-                        next = min(next, max(low + 26u, vref));
-                    }
-                    const uint32_t up = next - vref;
-                    vref = next;
-                    // PASSES: in two steps, since no factor below 2^-126 is normal
-                    const float fade = ex2_approx(-static_cast<float>(PASSES ? up / 2u : up));
-                    const float rest =
-                        PASSES ? ex2_approx(-static_cast<float>(up - up / 2u)) : 1.0f;
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                acc[i][nt][k] *= fade;
-                                if constexpr (PASSES) acc[i][nt][k] *= rest;
-                            }
-                }
-                if constexpr (PASSES) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const uint32_t taken = e[x] & __vcmpleu2(e[x], vref * 0x00010001u);
-                        vs[0][x] = relative_power2(taken, reference2(vref));
-                        e[x] ^= taken;         // those above the reference wait
-                    }
-                    again = __any_sync(0xFFFFFFFFu, (e[0] | e[1] | e[2] | e[3]) != 0u);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) vs[0][x] = relative_power2(e[x], reference2(vref));
-                }
-            }
-            uint32_t vraw[8][VW];
-#pragma unroll
-            for (uint32_t x = 0; x < 8; ++x)
-                load_shared(mine + tile_at + v_at[x % kCycle] + x / kCycle * 128u, vraw[x]);
-#pragma unroll
-            for (int w = 0; w < VW; ++w) {
-#pragma unroll
-                for (int ks2 = 0; ks2 < 2; ++ks2) {
-                    // even and odd elements of token pairs (x, x + 4), x = 2 ks2 and 2 ks2 + 1
-                    uint32_t even[2][4], odd[2][4];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t x = vraw[2 * ks2 + h][w], y = vraw[2 * ks2 + h + 4][w];
-                        decode_e2m1x8((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), even[h]);
-                        decode_e2m1x8(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), odd[h]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            even[h][i] = hmul2(even[h][i], vs[8 * w / G][2 * ks2 + h]);
-                            odd[h][i] = hmul2(odd[h][i], vs[8 * w / G][2 * ks2 + h]);
+                if constexpr (G == 32) {
+                    uint32_t top = __vimax3_u16x2(e[0], e[1], vref * 0x00010001u);
+                    top = __vimax3_u16x2(e[2], e[3], top);
+                    if (__any_sync(0xFFFFFFFFu, top != vref * 0x00010001u)) {
+                        uint32_t next = larger_half(top);
+                        next = max(next, __shfl_xor_sync(0xFFFFFFFFu, next, 1));
+                        next = max(next, __shfl_xor_sync(0xFFFFFFFFu, next, 2));
+                        if constexpr (PASSES) {    // by no more than keeps the smallest scale
+                            uint32_t low = smallest_half(e);
+                            low = min(low, __shfl_xor_sync(0xFFFFFFFFu, low, 1));
+                            low = min(low, __shfl_xor_sync(0xFFFFFFFFu, low, 2));
+                            next = min(next, max(low + 26u, vref));
                         }
+                        const uint32_t up = next - vref;
+                        vref = next;
+                        // PASSES: in two steps, since no factor below 2^-126 is normal
+                        const float fade = ex2_approx(-static_cast<float>(PASSES ? up / 2u : up));
+                        const float rest =
+                            PASSES ? ex2_approx(-static_cast<float>(up - up / 2u)) : 1.0f;
+#pragma unroll
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    acc[i][nt][k] *= fade;
+                                    if constexpr (PASSES) acc[i][nt][k] *= rest;
+                                }
                     }
+                    if constexpr (PASSES) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                        for (int x = 0; x < 4; ++x) {
+                            const uint32_t taken = e[x] & __vcmpleu2(e[x], vref * 0x00010001u);
+                            vs[0][x] = relative_power2(taken, reference2(vref));
+                            e[x] ^= taken;         // those above the reference wait
+                        }
+                        again = __any_sync(0xFFFFFFFFu, (e[0] | e[1] | e[2] | e[3]) != 0u);
+                    } else {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816(acc[4 * w + i][nt], even[0][i], odd[0][i], even[1][i],
-                                     odd[1][i], weights[nt][2 * ks2], weights[nt][2 * ks2 + 1]);
+                        for (int x = 0; x < 4; ++x)
+                            vs[0][x] = relative_power2(e[x], reference2(vref));
+                    }
                 }
-            }
+                uint32_t vraw[8][VW];
+#pragma unroll
+                for (uint32_t x = 0; x < 8; ++x)
+                    load_shared(mine + tile_at + v_at[x % kCycle] + x / kCycle * 128u, vraw[x]);
+#pragma unroll
+                for (int w = 0; w < VW; ++w) {
+#pragma unroll
+                    for (int ks2 = 0; ks2 < 2; ++ks2) {
+                        // even and odd elements of token pairs (x, x + 4), x = 2 ks2, 2 ks2 + 1
+                        uint32_t even[2][4], odd[2][4];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t x = vraw[2 * ks2 + h][w], y = vraw[2 * ks2 + h + 4][w];
+                            decode_e2m1x8((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), even[h]);
+                            decode_e2m1x8(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), odd[h]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                even[h][i] = hmul2(even[h][i], vs[8 * w / G][2 * ks2 + h]);
+                                odd[h][i] = hmul2(odd[h][i], vs[8 * w / G][2 * ks2 + h]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816(acc[4 * w + i][nt], even[0][i], odd[0][i], even[1][i],
+                                         odd[1][i], weights[nt][2 * ks2], weights[nt][2 * ks2 + 1]);
+                    }
+                }
             } while (PASSES && again);
         };
         if (edge) body(std::true_type{});
@@ -1007,8 +1009,8 @@ __global__ void __launch_bounds__(attention_warps(D) * 32, attention_blocks(D, N
         const uint32_t place = 2u * blockIdx.x + (share.at == first ? 0u : 1u);
         const uint32_t head = unit / p.row_tiles;
         attend<In, G, D, NT, MULTI>(p, smem, share.b, head, unit - head * p.row_tiles, n,
-                             piece * kPieceKeys, min(n, (piece + taken) * kPieceKeys),
-                             taken == pieces, place);
+                                    piece * kPieceKeys, min(n, (piece + taken) * kPieceKeys),
+                                    taken == pieces, place);
         // the block that holds a unit's first piece says where its parts are: its own
         // place, then one in every share up to the last that begins before the unit's end
         if (piece == 0u && threadIdx.x == 0u && p.joins != nullptr) {

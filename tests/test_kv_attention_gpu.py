@@ -335,6 +335,22 @@ def test_huge_values_of_many_keys(lens):
     compare(out, lse, want, "bf16", lens)
 
 
+@pytest.mark.parametrize("lens", [[100, 40], [700, 5000], [900] * 300])
+@pytest.mark.parametrize("low,high", [(170, 177), (165, 185), (230, 250)])
+def test_large_values_beside_larger_ones(lens, low, high):
+    """Warps and parts that have met scales of 2^50 and more, which move a power of two to their
+    reference, joined with others that have not."""
+    c, table = build(lens, 32, 1, 128, "mxfp4", spread=(low, low + 2))
+    c.k_scales.fill_(120)
+    for b, n in enumerate(lens):                          # every third page
+        pages = table[b, :n // 32:3].long()
+        c.v_scales[pages] += high - low
+    q = torch.randn(len(lens), 4, 128, device="cuda").bfloat16()
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    out, lse = pqg.kv_attention(q, c, table, n, return_lse=True)
+    compare(out, lse, reference(q, c, table, lens, 1, 128 ** -0.5), "bf16", lens)
+
+
 @pytest.mark.parametrize("sign", [-1.0, 1.0])
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 def test_huge_scores(fmt, sign):
@@ -420,6 +436,23 @@ def test_hidden_values_do_not_touch_a_row(D, Hq, q_len, newest, before):
     n = torch.tensor(lens, dtype=torch.int32, device="cuda")
     out, lse = pqg.kv_attention(q, c, table, n, return_lse=True)
     compare(out, lse, reference(q, c, table, lens, q_len, D ** -0.5), "bf16", lens)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("byte", [227, 255])
+def test_hidden_keys_do_not_touch_a_row(D, byte):
+    """The newest token's key has scales of 2^100, or the byte of no scale: rows of the tokens before
+    it are those of their own keys, to the bit."""
+    lens, q_len, P = [7, 64, 129, 700], 4, 32
+    c, table = build(lens, P, 2, D, "mxfp4")
+    q = torch.randn(len(lens) * q_len, 6, D, device="cuda").to(torch.bfloat16)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = pqg.kv_attention(q, c, table, n, return_lse=True)
+    for b, length in enumerate(lens):
+        c.k_scales[int(table[b, (length - 1) // P]), :, :, (length - 1) % P] = byte
+    got = pqg.kv_attention(q, c, table, n, return_lse=True)
+    older = torch.arange(len(q), device="cuda") % q_len < q_len - 1
+    assert all(torch.equal(a[older], b[older]) for a, b in zip(got, want))
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
