@@ -43,9 +43,10 @@ int make_plan(const CacheView &c, int64_t max_pages, int64_t B, int64_t q_len, i
     plan->shares = plan->units >= wave || pieces >= wave ? wave
                                                          : std::min(wave, plan->units * pieces);
     plan->split = cap > kPieceKeys;
-    // pieces are counted in 32 bits, rows of the join in 31
-    if (plan->units * ((cap + kPieceKeys - 1) / kPieceKeys) >= (int64_t{1} << 32) ||
-        B * c.heads * plan->rows >= (int64_t{1} << 31) - 4)
+    // rows of the join are counted in 31 bits (so units are, and the product below fits 64),
+    // pieces in 32
+    if (B * c.heads * plan->rows >= (int64_t{1} << 31) - 4 ||
+        plan->units * ((cap + kPieceKeys - 1) / kPieceKeys) >= (int64_t{1} << 32))
         return PQG_ERR_INVALID_ARG;
     plan->workspace = 0;
     if (plan->split && B > 0)

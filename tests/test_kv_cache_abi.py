@@ -171,3 +171,15 @@ def test_attention_nothing_to_do_and_scratch():
     assert work(cache(), 4096, 2, 1, 8, 100) > 0                    # the hint is no promise
     assert work(cache(), 4096, 0, 1, 8, 0) == 0
     assert work(cache(), 4096, 2, 1, 7, 0) == INV
+
+
+@host_only
+def test_attention_rejects_the_largest_sizes():
+    """Every size at its own limit: counts of rows and pieces that pass 64 bits when multiplied."""
+    c = cache(kv_heads=1024, num_pages=1)
+    kw = dict(B=1 << 20, q_len=1024, q_heads=16384, q_stride=1 << 30, max_pages=1 << 30,
+              table_stride=1 << 30)
+    before = pqg.pqg_launch_count()
+    assert attend(c, **kw) == INV
+    assert pqg.pqg_kv_attention_workspace(c, 1 << 30, 1 << 20, 1024, 16384, 0) == INV
+    assert pqg.pqg_launch_count() == before
