@@ -386,9 +386,9 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
  * pqg_kv_attention — attention of the last q_len tokens of B sequences over
  * the cache (decode: q_len = 1; several tokens: verification of drafts; a
  * chunk of some 200 tokens or more is faster with pqg_kv_read and a 16-bit
- * attention).  The tokens' own keys and values are in the cache already.  With n = seq_lens[b],
- * clamped into [0, max_pages * page_size], token t of sequence b sees keys
- * j < n - (q_len - 1 - t):
+ * attention).  The tokens' own keys and values are in the cache already.
+ * With n = seq_lens[b], clamped into [0, max_pages * page_size], token t of
+ * sequence b sees keys j < n - (q_len - 1 - t):
  *   s_j = sm_scale * sum_d q_d K_jd,  out = sum_j softmax(s)_j V_j,
  *   lse = log sum_j exp(s_j)
  * A row that sees no key has out = 0 and lse = -infinity.  Keys in a page that
@@ -415,17 +415,18 @@ PQG_API int pqg_kv_read(const pqg_kv_cache *cache, const int32_t *page_table,
  *          16-byte aligned (NULL when that is 0).  Its contents are dead
  *          after the call; calls that may run at the same time need one each.
  * Precision.  Sums are in fp32.  Keys and values enter the products exactly,
- * except that (MXFP4) a group of keys with scale byte 0 counts as zero, and so
- * does a group of values whose scale is 2^-27 or less of the largest one of
- * the same elements among the keys that the row sees; keys that it does not
- * see never touch it.  An element of a query is off by up to 2^-39 of the largest one
- * of its row (and head), which is exact down to 2^-31 (bf16) or 2^-28 (fp16)
- * of it.  The softmax weights are rounded for the product with V, to 11 bits
- * or by up to 2^-36 of the row's largest weight where that is more; the sum
- * that divides them is of the weights as they were.  Keys' scales from 2^118
- * on may give a score that is not finite, and values from 2^80 on a result
- * that is not where scores pass 2^22 in size.  A row whose query holds a NaN
- * has out and lse NaN, once it sees a key; other rows are not touched by it.
+ * except that (MXFP4) a group with scale byte 0, which pqg_kv_write does not
+ * make, may count as zero, and so may a group of values whose scale is 2^-27
+ * or less of the largest one of the same elements among the keys that the row
+ * sees; keys that it does not see never touch it.  An element of a query is
+ * off by up to 2^-39 of the largest one of its row (and head), and exact down
+ * to 2^-31 (bf16) or 2^-28 (fp16) of it.  The softmax weights are rounded for
+ * the product with V, to 11 bits or by up to 2^-36 of the row's largest weight
+ * where that is more; the sum that divides them is of the weights as they
+ * were.  Keys' scales from 2^118 on may give a score that is not finite, and
+ * values from 2^80 on a result that is not where scores pass 2^22 in size.  A
+ * row whose query holds a NaN has out and lse NaN, once it sees a key; other
+ * rows are not touched by it.
  * Results are the same for the same arguments (no atomics), max_len and the
  * number of the device's SMs included.  The other sequences of a call are
  * among them: how the keys are split goes by all lengths, so the last bits of
